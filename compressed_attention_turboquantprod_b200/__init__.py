@@ -14,8 +14,8 @@ from typing import Optional
 
 import torch
 
-__all__ = ["native", "TQError", "Codebook", "Projections", "CompressedKVCache", "LayerGroups",
-           "key_variance", "stack_partials", "gather_partials", "merge_partials"]
+__all__ = ["native", "TQError", "Codebook", "Projections", "CompressedKVCache", "PagedKVCache",
+           "LayerGroups", "key_variance", "stack_partials", "gather_partials", "merge_partials"]
 
 
 def __getattr__(name):
@@ -204,6 +204,180 @@ class CompressedKVCache:
                                    cb.centroids if cb is not None else None, out, logits,
                                    num_splits, ws)
         return (out, logits) if want_logits else out
+
+
+class PagedKVCache:
+    """Keys and values in 8 bits, in pages of `page` tokens with one scale per page and KV head;
+    sequences of any lengths, named by slots 0 .. slots-1, that fork, copy and free.
+
+    Slots and offsets are int32 CUDA tensors: row i of a call is slot slots[i] with the packed
+    tokens cu[i] .. cu[i+1]-1 (token-major [tokens, heads, d]).  Checks that need the state on
+    the device report through check(); see tq.h."""
+
+    CODES = {"int8": 0, "e4m3": 1}
+
+    def __init__(self, Hkv, d, pages, slots, max_pages, page: int = 64, code: str = "int8",
+                 dtype=torch.bfloat16, layers: int = 1, device="cuda"):
+        if code not in self.CODES:
+            raise ValueError(f"code {code!r} is not one of {sorted(self.CODES)}")
+        self.desc = native.make_paged_desc(layers, Hkv, d, page, pages, slots, max_pages, dtype,
+                                           self.CODES[code])
+        self.dtype = dtype
+        nbytes = native.tq_paged_bytes(self.desc)
+        if nbytes == 0:
+            native.tq_paged_layout(self.desc)      # raises with the reason
+        self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.state = native.tq_paged()
+        with torch.cuda.device(self.buffer.device):
+            native.tq_paged_init(self.state, self.desc, self.buffer)
+        self._ws = {}
+
+    def _on(self, *tensors):
+        """The cache's device made current; every tensor of the call has to be on it."""
+        for t in tensors:
+            if t is not None and t.device != self.buffer.device:
+                raise ValueError(f"tensor on {t.device}, the cache is on {self.buffer.device}")
+        return torch.cuda.device(self.buffer.device)
+
+    def _typed(self, *tensors):
+        for t in tensors:
+            if t.dtype != self.dtype:
+                raise ValueError(f"expected {self.dtype}, got {t.dtype}")
+
+    def workspace(self) -> torch.Tensor:
+        """The attention workspace of the current stream (calls on different streams may run
+        at the same time, so each has its own).  In a capture: one of the graph's own, made
+        ready by the graph itself."""
+        if torch.cuda.is_current_stream_capturing():
+            return self.make_workspace()
+        key = torch.cuda.current_stream(self.buffer.device).cuda_stream
+        if key not in self._ws:
+            self._ws[key] = self.make_workspace()
+        return self._ws[key]
+
+    def make_workspace(self) -> torch.Tensor:
+        """A new workspace, for attend(workspace=...)."""
+        with torch.cuda.device(self.buffer.device):
+            ws = torch.empty(native.tq_paged_workspace_bytes(self.state), dtype=torch.uint8,
+                             device=self.buffer.device)
+            native.tq_paged_workspace_init(self.state, ws)
+        return ws
+
+    # ---- tokens in, floats out
+    def extend(self, slots: torch.Tensor, cu: torch.Tensor):
+        """Take pages for cu[i+1]-cu[i] new tokens of each slot; then write() every layer."""
+        with self._on(slots, cu):
+            native.tq_paged_extend(self.state, slots, cu)
+
+    def write(self, K: torch.Tensor, V: torch.Tensor, layer: int = 0):
+        """The tokens of the last extend(), quantised into `layer`."""
+        self._typed(K, V)
+        with self._on(K, V):
+            native.tq_paged_write(self.state, layer, K, V)
+
+    def append(self, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, cu: torch.Tensor):
+        """extend() and write() of a cache of one layer."""
+        if self.desc.layers != 1:
+            raise ValueError("a cache of several layers takes extend() and a write() per layer")
+        self._typed(K, V)
+        with self._on(K, V, slots, cu):
+            native.tq_paged_extend(self.state, slots, cu)
+            native.tq_paged_write(self.state, 0, K, V)
+
+    def read(self, slots: torch.Tensor, cu: torch.Tensor, total: int, layer: int = 0):
+        """The first cu[i+1]-cu[i] tokens of each slot as floats: (K, V), [total, Hkv, d]."""
+        K, V = (torch.empty(total, self.desc.Hkv, self.desc.d, dtype=self.dtype,
+                            device=self.buffer.device) for _ in range(2))
+        with self._on(slots, cu):
+            native.tq_paged_read(self.state, layer, slots, cu, K, V)
+        return K, V
+
+    # ---- attention
+    def attend(self, Q: torch.Tensor, slots: torch.Tensor, cu: torch.Tensor, max_q: int,
+               causal: bool = True, softmax_scale: Optional[float] = None, layer: int = 0,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None):
+        """Row i's queries Q[cu[i]:cu[i+1]] over the tokens of slots[i].  causal: they are the
+        sequence's last tokens, each sees the tokens up to itself.  out and lse (float32
+        [tokens, Hq], log-sum-exp of the scaled logits) may be given."""
+        tokens, Hq, d = Q.shape
+        self._typed(Q)
+        scale = 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale
+        if out is None:
+            out = torch.empty(tokens, Hq, d, dtype=self.dtype, device=Q.device)
+        elif out.shape != Q.shape or out.dtype != self.dtype:
+            raise ValueError("out must have Q's shape and dtype")
+        if lse is not None and (lse.shape != (tokens, Hq) or lse.dtype != torch.float32):
+            raise ValueError("lse must be float32 [tokens, Hq]")
+        with self._on(Q, slots, cu, out, lse):
+            ws = self.workspace() if workspace is None else workspace
+            native.tq_paged_attention(self.state, layer, Q, slots, cu, max_q, causal, scale, out,
+                                      lse, ws)
+        return out
+
+    def _ones(self, n: int) -> torch.Tensor:
+        return torch.arange(n + 1, dtype=torch.int32, device=self.buffer.device)
+
+    def decode(self, Q: torch.Tensor, slots: torch.Tensor, softmax_scale: Optional[float] = None,
+               layer: int = 0, cu: Optional[torch.Tensor] = None, **kw):
+        """One query per slot, Q [n, Hq, d], over all of its tokens."""
+        cu = self._ones(slots.numel()) if cu is None else cu
+        return self.attend(Q, slots, cu, 1, True, softmax_scale, layer, **kw)
+
+    def decode_step(self, K: torch.Tensor, V: torch.Tensor, Q: torch.Tensor, slots: torch.Tensor,
+                    cu: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None, **kw):
+        """append() one token per slot (K, V [n, Hkv, d]), then decode()."""
+        cu = self._ones(slots.numel()) if cu is None else cu
+        self.append(K, V, slots, cu)
+        return self.decode(Q, slots, softmax_scale, cu=cu, **kw)
+
+    def cross(self, Q: torch.Tensor, slots: torch.Tensor, cu: torch.Tensor, max_q: int,
+              softmax_scale: Optional[float] = None, layer: int = 0, **kw):
+        """Cross attention: the slots hold an encoder's states, every query sees all of them."""
+        return self.attend(Q, slots, cu, max_q, False, softmax_scale, layer, **kw)
+
+    # ---- pages
+    def fork(self, src: torch.Tensor, dst: torch.Tensor):
+        """Sequence src[i] also becomes dst[i] (an empty slot); full pages are shared."""
+        with self._on(src, dst):
+            native.tq_paged_fork(self.state, src, dst)
+
+    def copy(self, src: torch.Tensor, dst: torch.Tensor, to: Optional["PagedKVCache"] = None):
+        """Sequence src[i] copied to the empty slot dst[i] of `to` (default: this cache)."""
+        other = self if to is None else to
+        if other.buffer.device != self.buffer.device:
+            raise ValueError("the caches are on different devices")
+        with self._on(src, dst):
+            native.tq_paged_copy(self.state, other.state, src, dst)
+
+    def free(self, slots: torch.Tensor):
+        with self._on(slots):
+            native.tq_paged_free(self.state, slots)
+
+    def compact(self):
+        """Move the live pages to the front of the pool."""
+        with self._on():
+            native.tq_paged_compact(self.state)
+
+    def page_table(self, slots: torch.Tensor) -> torch.Tensor:
+        """int32 [n, max_pages]: the pages of each slot, -1 where it has none."""
+        out = torch.empty(slots.numel(), self.desc.max_pages, dtype=torch.int32,
+                          device=self.buffer.device)
+        with self._on(slots):
+            native.tq_paged_table(self.state, slots, out)
+        return out
+
+    @property
+    def lengths(self) -> torch.Tensor:
+        """int32 [slots], a view of the state on the device: tokens of each sequence."""
+        o = self.state.o_len
+        return self.buffer[o:o + 4 * self.desc.slots].view(torch.int32)
+
+    def check(self) -> int:
+        """Raise if a call failed a check on the device since the last check (waits for the
+        stream); returns the number of free pages."""
+        with self._on():
+            return native.tq_paged_check(self.state)
 
 
 # ----------------------------------------------------------------------------- sharded context

@@ -10,6 +10,7 @@
 #include <mutex>
 #include <string>
 
+#include "paged.cuh"
 #include "tq_internal.h"
 
 namespace {
@@ -188,6 +189,9 @@ int set_error(int status, const char* fmt, ...) {
   return status;
 }
 
+int clear_error() { return ok(); }
+bool fault_injected(const char* name) { return injected(name); }
+
 Geom geom_of(const tq_cache* c) {
   Geom g;
   const tq_cache_desc& d = c->desc;
@@ -254,7 +258,9 @@ int tq_debug_bounds_check(void) {
     int (*read)();
   } files[] = {{"quant_kernels", tq::bounds_flag_quant}, {"decode_kernels", tq::bounds_flag_decode},
                {"decode_mma", tq::bounds_flag_decode_mma}, {"decode_mma_wide", tq::bounds_flag_wide},
-               {"prefill_mma", tq::bounds_flag_prefill}, {"prefill_tc", tq::bounds_flag_prefill_tc}};
+               {"prefill_mma", tq::bounds_flag_prefill}, {"prefill_tc", tq::bounds_flag_prefill_tc},
+               {"paged_pages", tq::bounds_flag_paged_pages}, {"paged_quant", tq::bounds_flag_paged_quant},
+               {"paged_attn", tq::bounds_flag_paged_attn}};
   int first = 0;
   const char* where = "";
   for (const auto& f : files) {

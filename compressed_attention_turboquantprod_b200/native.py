@@ -54,6 +54,19 @@ class tq_layer_groups(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int32), ("bound", ctypes.c_int32 * 8), ("m", ctypes.c_int32 * 8)]
 
 
+class tq_paged_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("layers", "Hkv", "d", "page", "pages", "slots",
+                                              "max_pages", "dtype", "code")]
+
+
+class tq_paged(ctypes.Structure):
+    _fields_ = ([("desc", tq_paged_desc), ("base", ctypes.c_void_p), ("bytes", ctypes.c_size_t)] +
+                [(n, ctypes.c_int64) for n in ("sub_bytes", "block_bytes", "page_bytes", "o_state",
+                                               "o_len", "o_table", "o_ref", "o_claim", "o_rows",
+                                               "o_scan", "o_moves", "o_remap", "o_tail", "o_pool")] +
+                [("plan_rows", ctypes.c_int32)])
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libtq.so not built ({LIB_PATH}); run "
@@ -62,6 +75,7 @@ def _load() -> ctypes.CDLL:
     P, I, I64, F, SZ, U64 = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
                              ctypes.c_size_t, ctypes.c_uint64)
     C = ctypes.POINTER(tq_cache)
+    G, GD = ctypes.POINTER(tq_paged), ctypes.POINTER(tq_paged_desc)
     D = ctypes.POINTER(tq_cache_desc)
     sig = {
         "tq_last_error": (ctypes.c_char_p, []),
@@ -102,6 +116,21 @@ def _load() -> ctypes.CDLL:
                                         ctypes.POINTER(I)]),
         "tq_merge_partials": (I, [P, P, I64, I, I, I, P, P]),
         "tq_layer_groups_parse": (I, [ctypes.c_char_p, ctypes.c_char_p, ctypes.POINTER(tq_layer_groups)]),
+        "tq_paged_bytes": (SZ, [GD]),
+        "tq_paged_layout": (I, [GD, G]),
+        "tq_paged_init": (I, [G, GD, P, SZ, P]),
+        "tq_paged_extend": (I, [G, P, P, I, P]),
+        "tq_paged_write": (I, [G, I, P, P, I64, I64, I64, P]),
+        "tq_paged_read": (I, [G, I, P, P, I, I64, P, P, P]),
+        "tq_paged_table": (I, [G, P, I, P, P]),
+        "tq_paged_workspace_bytes": (SZ, [G]),
+        "tq_paged_workspace_init": (I, [G, P, SZ, P]),
+        "tq_paged_attention": (I, [G, I, P, I64, I, P, P, I, I, I64, I, F, P, P, P, SZ, P]),
+        "tq_paged_fork": (I, [G, P, P, I, P]),
+        "tq_paged_copy": (I, [G, G, P, P, I, P]),
+        "tq_paged_free": (I, [G, P, I, P]),
+        "tq_paged_compact": (I, [G, P]),
+        "tq_paged_check": (I, [G, ctypes.POINTER(ctypes.c_int32), P]),
         "tq_m_for_layer": (I, [ctypes.POINTER(tq_layer_groups), I]),
     }
     for name, (res, args) in sig.items():
@@ -317,6 +346,130 @@ def tq_merge_partials(part_ml, part_o, out, stream=None):
     rows, slots, d = part_o.shape
     _check(lib.tq_merge_partials(_ptr(part_ml), _ptr(part_o), rows, slots, d, dtype_code(out.dtype),
                                  _ptr(out), _stream(stream)), "tq_merge_partials")
+
+
+# ----------------------------------------------------------------------------- paged 8-bit cache
+TQ_CODE_INT8, TQ_CODE_E4M3 = 0, 1
+
+
+def make_paged_desc(layers, Hkv, d, page, pages, slots, max_pages, dtype, code) -> tq_paged_desc:
+    return tq_paged_desc(layers, Hkv, d, page, pages, slots, max_pages,
+                         dtype if isinstance(dtype, int) else dtype_code(dtype), code)
+
+
+def tq_paged_bytes(desc: tq_paged_desc) -> int:
+    return lib.tq_paged_bytes(ctypes.byref(desc))
+
+
+def tq_paged_layout(desc: tq_paged_desc) -> tq_paged:
+    c = tq_paged()
+    _check(lib.tq_paged_layout(ctypes.byref(desc), ctypes.byref(c)), "tq_paged_layout")
+    return c
+
+
+def tq_paged_init(cache: tq_paged, desc: tq_paged_desc, buf: torch.Tensor, stream=None):
+    _check(lib.tq_paged_init(ctypes.byref(cache), ctypes.byref(desc), _ptr(buf),
+                             buf.numel() * buf.element_size(), _stream(stream)), "tq_paged_init")
+
+
+def _tokens(t: torch.Tensor, heads: int, d: int):
+    """(pointer, token stride in elements) of a token-major [tokens, heads, d] tensor whose
+    tokens are contiguous (a view into a wider row, such as a fused projection, will do)."""
+    if t.dim() != 3 or t.shape[1:] != (heads, d):
+        raise ValueError(f"expected [tokens, {heads}, {d}], got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError("the heads of a token must be contiguous")
+    # one token, or none, has no stride of its own
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def _i32(t: torch.Tensor):
+    if t.dtype != torch.int32 or t.dim() != 1:
+        raise ValueError("slots and offsets are one-dimensional int32 tensors")
+    return _ptr(t)
+
+
+def _rows(slots: torch.Tensor, cu: torch.Tensor) -> int:
+    if cu.numel() != slots.numel() + 1:
+        raise ValueError(f"{slots.numel()} slots need {slots.numel() + 1} offsets, got {cu.numel()}")
+    return slots.numel()
+
+
+def tq_paged_extend(cache: tq_paged, slots, cu, stream=None):
+    _check(lib.tq_paged_extend(ctypes.byref(cache), _i32(slots), _i32(cu), _rows(slots, cu),
+                               _stream(stream)), "tq_paged_extend")
+
+
+def tq_paged_write(cache: tq_paged, layer: int, K, V, stream=None):
+    if K.shape[0] != V.shape[0]:
+        raise ValueError("K and V have different token counts")
+    (kp, ks), (vp, vs) = (_tokens(t, cache.desc.Hkv, cache.desc.d) for t in (K, V))
+    _check(lib.tq_paged_write(ctypes.byref(cache), layer, kp, vp, ks, vs, K.shape[0],
+                              _stream(stream)), "tq_paged_write")
+
+
+def tq_paged_read(cache: tq_paged, layer: int, slots, cu, K, V, stream=None):
+    _check(lib.tq_paged_read(ctypes.byref(cache), layer, _i32(slots), _i32(cu), _rows(slots, cu),
+                             K.shape[0], _ptr(K), _ptr(V), _stream(stream)), "tq_paged_read")
+
+
+def tq_paged_table(cache: tq_paged, slots, out, stream=None):
+    _check(lib.tq_paged_table(ctypes.byref(cache), _i32(slots), slots.numel(), _ptr(out),
+                              _stream(stream)), "tq_paged_table")
+
+
+def tq_paged_workspace_bytes(cache: tq_paged) -> int:
+    return lib.tq_paged_workspace_bytes(ctypes.byref(cache))
+
+
+def tq_paged_workspace_init(cache: tq_paged, workspace, stream=None):
+    _check(lib.tq_paged_workspace_init(ctypes.byref(cache), _ptr(workspace), _ws(workspace),
+                                       _stream(stream)), "tq_paged_workspace_init")
+
+
+def tq_paged_attention(cache: tq_paged, layer: int, Q, slots, cu, max_q: int, causal: bool,
+                       softmax_scale: float, out, lse, workspace, stream=None):
+    """Q [total_q, Hq, d] (token views as for K and V); out contiguous; lse or None."""
+    Hq = Q.shape[1]
+    qp, qs = _tokens(Q, Hq, cache.desc.d)
+    _check(lib.tq_paged_attention(ctypes.byref(cache), layer, qp, qs, Hq, _i32(slots), _i32(cu),
+                                  _rows(slots, cu), max_q, Q.shape[0], int(causal), softmax_scale,
+                                  _ptr(out), _ptr(lse), _ptr(workspace), _ws(workspace),
+                                  _stream(stream)), "tq_paged_attention")
+
+
+def _pairs(src, dst) -> int:
+    if src.numel() != dst.numel():
+        raise ValueError("as many sources as destinations are needed")
+    return src.numel()
+
+
+def tq_paged_fork(cache: tq_paged, src, dst, stream=None):
+    _check(lib.tq_paged_fork(ctypes.byref(cache), _i32(src), _i32(dst), _pairs(src, dst),
+                             _stream(stream)), "tq_paged_fork")
+
+
+def tq_paged_copy(cache: tq_paged, to_cache: tq_paged, src, dst, stream=None):
+    _check(lib.tq_paged_copy(ctypes.byref(cache), ctypes.byref(to_cache), _i32(src), _i32(dst),
+                             _pairs(src, dst), _stream(stream)), "tq_paged_copy")
+
+
+def tq_paged_free(cache: tq_paged, slots, stream=None):
+    _check(lib.tq_paged_free(ctypes.byref(cache), _i32(slots), slots.numel(), _stream(stream)),
+           "tq_paged_free")
+
+
+def tq_paged_compact(cache: tq_paged, stream=None):
+    _check(lib.tq_paged_compact(ctypes.byref(cache), _stream(stream)), "tq_paged_compact")
+
+
+def tq_paged_check(cache: tq_paged, stream=None) -> int:
+    """Raise if a call on the cache failed a device check since the last one (waits for the
+    stream; clears the status); returns the number of free pages."""
+    free = ctypes.c_int32()
+    _check(lib.tq_paged_check(ctypes.byref(cache), ctypes.byref(free), _stream(stream)),
+           "tq_paged_check")
+    return free.value
 
 
 # ----------------------------------------------------------------------------- layer groups

@@ -480,6 +480,173 @@ int tq_decode_attention_noalloc(const tq_cache* c, const void* Q, int Hq, float 
                                 void* out, float* logits, int num_splits, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* The paged 8-bit cache                                                     */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A second cache form beside tq_cache, for layers that need more than 1-4 bits
+ * and for batches whose sequences have lengths of their own: keys and values in
+ * 8 bits, in pages of `page` tokens, with one scale for each block (the tokens of
+ * a page in one KV head; keys and values apart).  With a the largest magnitude
+ * over the finite entries of a block:
+ *   TQ_CODE_INT8  code = round-half-even(127 x / a), scale = fl32(a / 127)
+ *   TQ_CODE_E4M3  scale = the smallest 2^k with a / scale <= 448,
+ *                 code = e4m3(x / scale), round half even
+ * and an entry stands for code * scale.  A block with a < 2^-100 is stored as
+ * zeros, an infinity saturates, a NaN is stored as 0.  The last, partly filled
+ * page of a sequence keeps its tokens exactly as well (the tail), so its codes are
+ * always those of the exact tokens present, however they were appended; a full
+ * page never changes again.
+ *
+ * Sequences are `slots` (0 .. slots-1), rows of a page table on the device; pages
+ * carry reference counts and are taken lowest first.  All of this state lives in
+ * the caller's buffer on the device: no call needs the host to know a length, and
+ * every call can be captured into a CUDA graph and replayed.  What only the device
+ * can check (free pages, slots, offsets) is checked there: a call that fails such
+ * a check leaves the cache as it was (tq_paged_write then writes nothing), sets a
+ * sticky status and goes on; tq_paged_check reads it.
+ * Calls that change a cache must be ordered with each other and with its readers
+ * (one stream, or events); readers may overlap, each with its own workspace.
+ * Several layers share the page table: tq_paged_extend once, then tq_paged_write
+ * for each layer.
+ */
+enum tq_code { TQ_CODE_INT8 = 0, TQ_CODE_E4M3 = 1 };
+
+typedef struct tq_paged_desc {
+  int32_t layers;     /* layers that share the page table, 1..1024           */
+  int32_t Hkv;        /* KV heads, 1..1024                                   */
+  int32_t d;          /* head dim: 64, 128 or 256                            */
+  int32_t page;       /* tokens per page: 16, 32, 64 or 128                  */
+  int32_t pages;      /* pages in the pool, 1..2^20                          */
+  int32_t slots;      /* sequences, 1..65536                                 */
+  int32_t max_pages;  /* pages a sequence may have; max_pages * page < 2^31  */
+  int32_t dtype;      /* dtype of K, V, Q, the tail and the output           */
+  int32_t code;       /* enum tq_code                                        */
+} tq_paged_desc;
+
+/* Host handle of a paged cache: the layout of its buffer, plus the row count of
+ * the last tq_paged_extend (the grid size of tq_paged_write). */
+typedef struct tq_paged {
+  tq_paged_desc desc;
+  void* base;            /* caller-owned device buffer                        */
+  size_t bytes;
+  int64_t sub_bytes, block_bytes, page_bytes;   /* sub-block, block, page of one layer */
+  int64_t o_state, o_len, o_table, o_ref, o_claim, o_rows, o_scan, o_moves, o_remap,
+          o_tail, o_pool;
+  int32_t plan_rows;
+} tq_paged;
+
+/* Bytes of device memory a cache with this descriptor needs (0 if invalid). */
+size_t tq_paged_bytes(const tq_paged_desc* desc);
+
+/* Host only: fill `out` with the layout (base = NULL).  Errors: INVALID_ARG,
+ * UNSUPPORTED. */
+int tq_paged_layout(const tq_paged_desc* desc, tq_paged* out);
+
+/* Bind a device buffer of at least tq_paged_bytes(desc) bytes (256-byte aligned),
+ * empty every slot and free every page, on `stream`.  Errors: INVALID_ARG,
+ * UNSUPPORTED, CUDA. */
+int tq_paged_init(tq_paged* c, const tq_paged_desc* desc, void* dev_mem, size_t bytes, void* stream);
+
+/*
+ * tq_paged_extend -- take pages for new tokens: row i (0 <= i < n) appends
+ * cu[i+1] - cu[i] tokens to slot slots[i]; slot -1 is a padding row whose tokens
+ * are left out.  The new tokens become visible at once: write every layer
+ * (tq_paged_write) before attending.
+ *   slots  device int32[n], no slot twice;  cu  device int32[n+1], cu[0] >= 0, not
+ *          decreasing
+ *   n      1..desc.slots
+ * Device checks: CAPACITY (free pages; max_pages), INVALID_ARG (slots, offsets).
+ * Errors: INVALID_ARG, CUDA.
+ *
+ * tq_paged_write -- quantise the tokens of the last tq_paged_extend into layer
+ * `layer`: row i's tokens are K[cu[i]] .. K[cu[i+1]-1].
+ *   K, V     device [total][Hkv][d] of desc.dtype, token-major; token t starts at
+ *            element t * k_stride (v_stride), a multiple of 16 bytes and at least
+ *            Hkv * d (views into a fused projection need no copy)
+ *   total    tokens in K and V (0: nothing to do)
+ * Device checks: INVALID_ARG (an offset past `total`; that block is not written).
+ * Errors: INVALID_ARG, CUDA.
+ */
+int tq_paged_extend(tq_paged* c, const int32_t* slots, const int32_t* cu, int n, void* stream);
+int tq_paged_write(const tq_paged* c, int layer, const void* K, const void* V, int64_t k_stride,
+                   int64_t v_stride, int64_t total, void* stream);
+
+/*
+ * tq_paged_read -- the first cu[i+1] - cu[i] cached tokens of slot slots[i] as
+ * floats (code * scale rounded once to desc.dtype; zeros past the sequence's end)
+ * into K, V [total][Hkv][d] at tokens cu[i].. .  Rows outside [cu[0], cu[n]) are
+ * left as they were.  Errors: INVALID_ARG, CUDA.
+ */
+int tq_paged_read(const tq_paged* c, int layer, const int32_t* slots, const int32_t* cu, int n,
+                  int64_t total, void* K, void* V, void* stream);
+
+/* Device int32 out[n][max_pages] = the page table rows of the slots, -1 where a
+ * sequence has no page.  Errors: INVALID_ARG, CUDA. */
+int tq_paged_table(const tq_paged* c, const int32_t* slots, int n, int32_t* out, void* stream);
+
+/*
+ * tq_paged_attention -- queries over cached sequences: row i's queries are tokens
+ * cu[i] .. cu[i+1]-1 of Q, over the L tokens of slot slots[i] (a slot may be named
+ * by several rows; slot -1, or one out of range, is an empty sequence).
+ *   causal != 0: query j of n sees tokens 0 .. L - n + j (the last n tokens of the
+ *                sequence are the queries' own: append first, then attend)
+ *   causal == 0: every query sees all L tokens (cross attention: the sequence holds
+ *                an encoder's states, of a length of its own)
+ * out = sum_t p_t v_t, p = softmax(softmax_scale <q, k_t>) over the visible tokens;
+ * a query that sees none gives 0.  One query per sequence is the decode.
+ *   Q        device, token t's heads [Hq][d] at element t * q_stride (16-byte
+ *            aligned tokens, q_stride >= Hq * d), of desc.dtype
+ *   Hq       a multiple of Hkv, at most 8 Hkv
+ *   cu       device int32[n+1], not decreasing; max_q >= every cu[i+1] - cu[i]
+ *   total_q  tokens in Q and out; tokens outside [cu[0], cu[n]) are left as they were
+ *   out      device [total_q][Hq][d] of desc.dtype (written)
+ *   lse      device float[total_q][Hq]: log sum exp of the scaled logits (-inf where
+ *            nothing is visible), or NULL
+ *   workspace  device, 256-byte aligned, tq_paged_workspace_bytes(c) bytes, made
+ *            ready once by tq_paged_workspace_init; every call leaves it ready.
+ *            Calls that may run at the same time need workspaces of their own
+ * Device checks: INVALID_ARG (workspace not made ready; a row longer than max_q).
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+size_t tq_paged_workspace_bytes(const tq_paged* c);
+int tq_paged_workspace_init(const tq_paged* c, void* workspace, size_t ws_bytes, void* stream);
+int tq_paged_attention(const tq_paged* c, int layer, const void* Q, int64_t q_stride, int Hq,
+                       const int32_t* slots, const int32_t* cu, int n, int max_q, int64_t total_q,
+                       int causal, float softmax_scale, void* out, float* lse, void* workspace,
+                       size_t ws_bytes, void* stream);
+
+/*
+ * Page management.  Arrays are device int32.
+ * tq_paged_fork -- sequence from[i] also becomes sequence to[i]: full pages are
+ *   shared (their count rises), the partly filled page and the tail are copied, so
+ *   that both go on independently.  One source may have many forks; destinations are
+ *   distinct, empty, and no source of the same call.
+ * tq_paged_copy -- the same with every page copied; `src` may be another cache of
+ *   the same layers, Hkv, d, page, dtype and code on the same device.
+ * tq_paged_free -- empty the slots; a page whose count falls to 0 is free.  Slot -1
+ *   is skipped, an empty slot stays empty.
+ * tq_paged_compact -- move the live pages at or beyond the number of live pages into
+ *   the free ones below it (both in ascending order) and renumber the page tables:
+ *   afterwards pages 0 .. live-1 are in use and the rest of the pool is free.
+ * Device checks: CAPACITY (free pages, max_pages), INVALID_ARG (slots, destination
+ * not empty).  Errors: INVALID_ARG, CUDA.
+ */
+int tq_paged_fork(tq_paged* c, const int32_t* from, const int32_t* to, int n, void* stream);
+int tq_paged_copy(const tq_paged* src, tq_paged* dst, const int32_t* from, const int32_t* to, int n,
+                  void* stream);
+int tq_paged_free(tq_paged* c, const int32_t* slots, int n, void* stream);
+int tq_paged_compact(tq_paged* c, void* stream);
+
+/*
+ * tq_paged_check -- SYNCHRONOUS: waits for `stream`, then reports (and clears) the
+ * sticky status of the cache: CAPACITY, INVALID_ARG or CUDA (a bounded wait gave
+ * up) with the reason in tq_last_error(); free_pages (may be NULL) receives the
+ * number of free pages.
+ */
+int tq_paged_check(tq_paged* c, int32_t* free_pages, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Adaptive per-layer-group sketch dimension ([AQJL] A-QJL, deployment)     */
 /* ------------------------------------------------------------------------ */
 
