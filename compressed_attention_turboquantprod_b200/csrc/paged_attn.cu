@@ -1,15 +1,15 @@
 // Attention over the paged 8-bit cache: decode, causal chunks, cross attention.
 // logit = scale <q, k>, p = softmax over the visible tokens, out = sum p v, k and v the
 // values the codes stand for.
-#include <cuda_fp8.h>
-
+#include "mma_common.cuh"
 #include "paged.cuh"
 
 namespace tq {
 namespace {
+using namespace mmadec;
 
 // A workspace begins with this word (tq_paged_workspace_init), so that one that was never made
-// ready is reported instead of used.
+// ready is reported instead of used; the counters behind it are zero between calls.
 constexpr uint32_t kWsMagic = 0x70384b56u;
 constexpr size_t kWsHeader = 4096;
 
@@ -18,79 +18,664 @@ __global__ void k_paged_ws_init(uint32_t* ws) {
   for (int i = threadIdx.x; i < (int)(kWsHeader / 4); i += blockDim.x) ws[i] = i == 0 ? kWsMagic : 0u;
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
+// ---------------------------------------------------------------- the split over CTAs
+// The work of a call is a list of tiles of 64 tokens, in the order (sequence, group of query
+// rows, head, tile); a unit is one (sequence, group, head), at least one tile long so that a
+// unit that sees nothing is also written.  Every CTA takes an equal, contiguous share of the
+// list, whatever the lengths: a CTA's share may begin and end inside a unit, and then leaves a
+// partial (m, l, o) for the CTA that finishes that unit last.  Lengths are read on the device,
+// so a captured call follows them.
+constexpr int kTile = 64;
 
-__device__ __forceinline__ float byte_value(uint32_t u, int code) {
-  if (code == TQ_CODE_INT8) return (float)((int)u - 128);
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)u, __NV_E4M3)));
+struct Seq {
+  int slot, len, nq, q0;
+};
+
+__device__ __forceinline__ Seq load_seq(const PGeom& g, const PagedAttn& a, int i) {
+  Seq s;
+  s.slot = a.slots[i];
+  s.q0 = a.cu[i];
+  s.nq = min(max(a.cu[i + 1] - s.q0, 0), a.max_q);
+  s.len = paged_len(g, s.slot);
+  return s;
 }
 
-// One warp per (query token, head), a token at a time: the form every other is held against.
+// Tokens that query j of the sequence sees.
+__device__ __forceinline__ int visible(const Seq& s, int j, int causal) {
+  return causal ? max(0, min(s.len, s.len - s.nq + j + 1)) : s.len;
+}
+
+// Row groups of R rows (row r: query r / G, head r mod G of the KV head) and their tiles.
+template <int R>
+__device__ __forceinline__ int seq_groups(const Seq& s, int G) {
+  return (int)(((int64_t)s.nq * G + R - 1) / R);
+}
+template <int R>
+__device__ __forceinline__ int group_visible(const Seq& s, int G, int rg, int causal) {
+  return visible(s, (int)(min((int64_t)(rg + 1) * R, (int64_t)s.nq * G) - 1) / G, causal);
+}
+template <int R, int T>
+__device__ __forceinline__ int group_tiles(const Seq& s, int G, int rg, int causal) {
+  return max(1, (group_visible<R>(s, G, rg, causal) + T - 1) / T);
+}
+
+// Whether this thread of CTA 0 found a row with offsets that decrease or pass max_q or total_q.
+__device__ __forceinline__ bool cta_first_checks(const PGeom& g, const PagedAttn& a) {
+  bool bad = false;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
+      const int b = a.cu[i], e = a.cu[i + 1];
+      bad |= b < 0 || e < b || e > a.total_q || e - b > a.max_q;
+    }
+  return bad;
+}
+
+struct Cursor {      // a unit: its place in the list, and what it is
+  int64_t u0;
+  int nt, i, rg, h;
+  Seq s;
+};
+
+// Tiles of sequence i, by one thread: a causal sequence's groups see one run of lengths.
+template <int R, int T>
+__device__ int64_t seq_tiles(const PGeom& g, const PagedAttn& a, int i, int G) {
+  const Seq s = load_seq(g, a, i);
+  const int ng = seq_groups<R>(s, G);
+  if (ng == 0) return 0;
+  if (!a.causal || s.nq == 1) return (int64_t)g.Hkv * ng * group_tiles<R, T>(s, G, 0, a.causal);
+  int64_t t = 0;
+  for (int rg = 0; rg < ng; ++rg) t += group_tiles<R, T>(s, G, rg, a.causal);
+  return g.Hkv * t;
+}
+
+// All threads of the CTA (NT): the number of tiles of the call.
+template <int R, int T, int NT>
+__device__ int64_t count_tiles(const PGeom& g, const PagedAttn& a, int G, int64_t* s_sum) {
+  int64_t t = 0;
+  for (int i = threadIdx.x; i < a.n; i += NT) t += seq_tiles<R, T>(g, a, i, G);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = t;
+  __syncthreads();
+  t = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) t += s_sum[w];
+  return t;
+}
+
+// One warp: the unit that holds tile x of the list.
+template <int R, int T>
+__device__ Cursor find_unit(const PGeom& g, const PagedAttn& a, int G, int64_t x) {
+  const int lane = threadIdx.x & 31;
+  int64_t base = 0;
+  Cursor c{};
+  int i = 0;
+  for (int i0 = 0; i0 < a.n; i0 += 32) {
+    const int64_t t = i0 + lane < a.n ? seq_tiles<R, T>(g, a, i0 + lane, G) : 0;
+    int64_t v = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + v > x);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      base += __shfl_sync(0xffffffffu, v - t, l);
+      i = i0 + l;
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, v, 31);
+  }
+  c.i = i;
+  c.s = load_seq(g, a, i);
+  const int ng = seq_groups<R>(c.s, G);
+  for (int r0 = 0; r0 < ng; r0 += 32) {
+    const int64_t t = r0 + lane < ng ? (int64_t)g.Hkv * group_tiles<R, T>(c.s, G, r0 + lane, a.causal) : 0;
+    int64_t v = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + v > x);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      base += __shfl_sync(0xffffffffu, v - t, l);
+      c.rg = r0 + l;
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, v, 31);
+  }
+  c.nt = group_tiles<R, T>(c.s, G, c.rg, a.causal);
+  c.h = (int)((x - base) / c.nt);
+  c.u0 = base + (int64_t)c.h * c.nt;
+  return c;
+}
+
+// The next unit of the list (the caller knows that there is one).
+template <int R, int T>
+__device__ __forceinline__ void next_unit(const PGeom& g, const PagedAttn& a, int G, Cursor& c) {
+  c.u0 += c.nt;
+  if (++c.h < g.Hkv) return;
+  c.h = 0;
+  if (++c.rg >= seq_groups<R>(c.s, G)) {
+    c.rg = 0;
+    do {
+      c.s = load_seq(g, a, ++c.i);
+    } while (c.s.nq == 0 && c.i + 1 < a.n);
+  }
+  c.nt = group_tiles<R, T>(c.s, G, c.rg, a.causal);
+}
+
+// CTAs that take part in W tiles (at least `least` tiles each), the first tile of CTA c, and
+// the CTA that holds tile x.
+__device__ __forceinline__ int64_t share_ctas(int64_t W, int ctas, int least) {
+  return max((int64_t)1, min((int64_t)ctas, (W + least - 1) / least));
+}
+__device__ __forceinline__ int64_t share_begin(int64_t W, int64_t C, int64_t c) { return W * c / C; }
+__device__ __forceinline__ int share_owner(int64_t W, int64_t C, int64_t x) { return (int)(((x + 1) * C - 1) / W); }
+
+// ---------------------------------------------------------------- decode
+// Up to 8 query rows of a KV head over its tokens, bound by reading the codes once.
+//
+// Both products run on warp-level m16n8k16 f16 MMA: 8 rows fill half an MMA, the other half
+// carries what rounding the first to 11 bits left over (q in rows 0-7, q - f16(q) in rows
+// 8-15, and p likewise), so that with exact f16 codes the products have 22 bits at no cost.
+// q is scaled by a power of two per row so that its largest entry is in [2^14, 2^15).
+//
+// A warp owns whole tiles of 64 tokens: `cp.async.bulk` brings a tile's key sub-blocks, then
+// its value sub-blocks, into the warp's own ring of stages; nothing in the loop waits for
+// another warp.  No operand is shuffled: MMA k indices may be permuted alike in A and B, so
+// lane (g, c) = (lane / 4, lane mod 4) reads 16 key bytes (channels 64 j + 16 c ...) of token
+// 16 (g / 2) + 2 i + (g mod 2) for column g of n-tile i; its scores are then those of tokens
+// 16 c + 2 i + {0, 1}: the 16 tokens whose value bytes are its one 16-byte read per channel.
+// Each tile's P V starts from zero and is added to the fp32 output in round-to-nearest (the
+// tensor core's own long sums truncate: 2^-25 a step, one way).
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecRows = 8;
+
 template <int D>
-__global__ void __launch_bounds__(128) k_paged_attn_plain(PGeom g, PagedAttn a) {
+struct DecCfg {
+  static constexpr int kCtas = D == 256 ? 1 : 2;              // resident CTAs per SM
+  static constexpr int kStages = D == 64 ? 5 : 3;             // half tiles (keys or values) in flight per warp
+};
+// A sub-block's place in a stage: padded so that the four lanes c of a value read, which are in
+// 64 / SUB sub-blocks, fall into different banks.
+template <int D, int SUB>
+__host__ __device__ constexpr int dec_sub_stride() { return SUB * D + 2 * SUB; }
+template <int D, int SUB>
+__host__ __device__ constexpr int dec_stage() { return kTile / SUB * dec_sub_stride<D, SUB>(); }
+template <int D, int SUB>
+__host__ __device__ constexpr size_t dec_smem() {
+  return (size_t)kDecWarps * DecCfg<D>::kStages * dec_stage<D, SUB>() + (D / 16) * 32 * 16 +
+         (kDecWarps / 2) * kDecRows * D * 4;
+}
+
+// 4 stored bytes -> two f16 pairs, exact.  int8: byte u under 0x64 is the half 1024 + u.
+template <int CODE>
+__device__ __forceinline__ void expand4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (CODE == TQ_CODE_INT8) {
+    const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));     // 1152
+    const uint32_t a = prmt(w, 0x64646464u, 0x4140), b = prmt(w, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Partials: [2 x CTAs][8] (m, l) and [2 x CTAs][8][D] o, after the workspace header.  CTA c
+// writes slot 2 c for a unit that began before it, 2 c + 1 for one that goes on after it.
+struct DecWs {
+  int* count;          // [CTAs] finished parts of the unit that goes on after CTA c
+  float2* ml;
+  float* o;
+};
+constexpr int kMaxCtas = 2 * 148;
+
+__host__ __device__ __forceinline__ DecWs dec_ws(void* ws) {
+  DecWs w;
+  unsigned char* p = static_cast<unsigned char*>(ws);
+  w.count = reinterpret_cast<int*>(p + 256);
+  w.ml = reinterpret_cast<float2*>(p + kWsHeader);
+  w.o = reinterpret_cast<float*>(p + kWsHeader + (size_t)2 * kMaxCtas * kDecRows * 8);
+  return w;
+}
+
+template <int D, int SUB, int CODE>
+__global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(PGeom g, PagedAttn a) {
+  constexpr int NST = DecCfg<D>::kStages, SS = dec_sub_stride<D, SUB>(), STB = dec_stage<D, SUB>();
+  constexpr int NSUB = kTile / SUB, KS = D / 16, NT = D / 8;
+  constexpr uint32_t kBytes = NSUB * (SUB * D + kPagedTrailer);
+  constexpr float kUp = 32768.f;           // p is held times 2^15: its halves reach 2^-40
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) uint64_t s_full[kDecWarps][NST];
+  __shared__ int64_t s_sum[kDecWarps];
+  __shared__ Cursor s_cur;
+  __shared__ float s_fr[kDecRows];
+  __shared__ int s_vis[kDecRows];
+  __shared__ float2 s_ml[kDecWarps][kDecRows];
+  __shared__ int s_abort, s_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gi = lane >> 2, c = lane & 3;
+  unsigned char* ring = smem + warp * (NST * STB);
+  uint4* s_q = reinterpret_cast<uint4*>(smem + kDecWarps * NST * STB);          // [KS][32] A fragments
+  float* s_o = reinterpret_cast<float*>(s_q + KS * 32);                         // [2 warps][8][D]
+  if (tid == 0) {
+    for (int w = 0; w < kDecWarps; ++w)
+      for (int s = 0; s < NST; ++s) mbar_init(&s_full[w][s], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_abort = 0;
+  }
   pdl_wait();
-  if (*static_cast<const uint32_t*>(a.ws) != kWsMagic) {
-    if (threadIdx.x == 0) atomicOr(&g.state->status, kPagedBadWorkspace);
+  pdl_launch_dependents();
+  const int G = a.Hq / g.Hkv;
+  if (*static_cast<const volatile uint32_t*>(a.ws) != kWsMagic) {
+    if (tid == 0) atomicOr(&g.state->status, kPagedBadWorkspace);
     return;
   }
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (w >= a.total_q * a.Hq) return;
-  const int64_t tok = w / a.Hq;
-  const int hq = (int)(w % a.Hq), h = hq / (a.Hq / g.Hkv);
-  if (tok >= a.cu[a.n] || tok < a.cu[0]) return;      // rows behind the last sequence stay
-  int i = 0;
-  for (int lo = 0, hi = a.n; hi - lo > 1;) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu[mid] <= tok) lo = mid; else hi = mid;
-    i = lo;
+  if (cta_first_checks(g, a)) atomicOr(&g.state->status, kPagedBadOffsets);
+  const int64_t W = count_tiles<kDecRows, kTile, kDecThreads>(g, a, G, s_sum);
+  if (W == 0) return;
+  const int64_t C = share_ctas(W, gridDim.x, kDecWarps);
+  const int cta = blockIdx.x;
+  if (cta >= C) return;
+  const int64_t x0 = share_begin(W, C, cta), x1 = share_begin(W, C, cta + 1);
+  if (warp == 0) {
+    const Cursor f = find_unit<kDecRows, kTile>(g, a, G, x0);
+    if (lane == 0) s_cur = f;
   }
-  const int slot = a.slots[i], len = paged_len(g, slot);
-  const int nq = a.cu[i + 1] - a.cu[i], qi = (int)(tok - a.cu[i]);
-  if (nq > a.max_q && lane == 0) atomicOr(&g.state->status, kPagedBadOffsets);
-  const int vis = a.causal ? max(0, min(len, len - nq + qi + 1)) : len;
-  constexpr int N = D / 32;
-  float q[N], o[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    q[k] = load_f(a.Q, tok * a.q_stride + (int64_t)hq * D + 32 * k + lane, g.dtype);
-    o[k] = 0.f;
+  __syncthreads();
+  Cursor cur = s_cur, nxt = cur;            // the unit at work, and that of the tile to request next
+  const DecWs ws = dec_ws(a.ws);
+
+  // ---- requests: tile x belongs to warp x mod 4; the page of the next one is read ahead
+  int64_t xi = x0 + ((warp - x0) & (kDecWarps - 1));
+  int nvis = 0, npid = 0, nsub = 0;
+  auto look = [&]() {                       // the tile at xi: its unit, and this lane's sub-block
+    nvis = 0;
+    if (xi >= x1) return;
+    while (xi >= nxt.u0 + nxt.nt) next_unit<kDecRows, kTile>(g, a, G, nxt);
+    nvis = group_visible<kDecRows>(nxt.s, G, nxt.rg, a.causal);
+    if (nvis > 0 && lane < NSUB) {
+      // sub-blocks past the end repeat the last one: masked, but finite
+      const int t = min((int)(xi - nxt.u0) * kTile + lane * SUB, nxt.s.len - 1);
+      npid = g.table[(int64_t)nxt.s.slot * g.max_pages + t / g.page];
+      nsub = t % g.page / SUB;
+    }
+  };
+  int ist = 0;                              // stage of the next request
+  auto request = [&](int kv) {
+    uint64_t* bar = &s_full[warp][ist];
+    if (lane == 0) mbar_expect_tx(bar, kBytes);
+    __syncwarp();
+    if (lane < NSUB) {
+      if ((unsigned)npid >= (unsigned)g.pages) {
+        atomicOr(&g.state->status, kPagedBadPage);
+        npid = 0;
+      }
+      cache_bulk_load(ring + ist * STB + lane * SS, paged_block(g, a.layer, npid, kv, nxt.h, nsub), SUB * D + kPagedTrailer,
+                      bar, g.base, g.total, 401);
+    }
+    ist = ist + 1 == NST ? 0 : ist + 1;
+  };
+  int half = 0;                             // 0: the keys of tile xi are next, 1: its values
+  auto refill = [&]() {
+    if (xi >= x1) return;
+    request(half);
+    half ^= 1;
+    if (half == 0) {
+      xi += kDecWarps;
+      look();
+      while (xi < x1 && nvis == 0) {        // nothing to load for a unit that sees nothing
+        xi += kDecWarps;
+        look();
+      }
+    }
+  };
+  look();
+  while (xi < x1 && nvis == 0) {
+    xi += kDecWarps;
+    look();
   }
-  float m = -INFINITY, l = 0.f;
-  for (int t = 0; t < vis; ++t) {
-    const int pid = g.table[(int64_t)slot * g.max_pages + t / g.page];
-    if ((unsigned)pid >= (unsigned)g.pages) continue;
-    const int si = t % g.page / g.sub, tb = t % g.page % g.sub;
-    const uint8_t* kb = paged_block(g, a.layer, pid, 0, h, si);
-    const uint8_t* vb = paged_block(g, a.layer, pid, 1, h, si);
-    float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < N; ++k) s = fmaf(q[k], byte_value(kb[paged_k_off(D, tb, 32 * k + lane)], g.code), s);
-    s = warp_sum(s) * *reinterpret_cast<const float*>(kb + g.sub * D) * a.scale;
-    const float mn = fmaxf(m, s), al = exp2f((m - mn) * kLog2e), p = exp2f((s - mn) * kLog2e);
-    const float sv = *reinterpret_cast<const float*>(vb + g.sub * D) * p;
+  for (int s = 0; s < NST; ++s) refill();
+  int cst = 0;
+  uint32_t cph = 0;
+  auto wait_stage = [&]() {
+    if (!s_abort && !mbar_wait(&s_full[warp][cst], cph)) {
+      s_abort = 1;
+      atomicOr(&g.state->status, kPagedWait);
+    }
+  };
+  auto next_stage = [&]() {
+    if (++cst == NST) {
+      cst = 0;
+      cph ^= 1;
+    }
+  };
+
+  int64_t x = x0;
+  while (x < x1) {
+    const int64_t ue = cur.u0 + cur.nt, xe = min(x1, ue);
+    // ---- the unit's queries as A fragments, two rows per warp
+    __syncthreads();
+    const int rows = (int)min((int64_t)kDecRows, (int64_t)cur.s.nq * G - (int64_t)cur.rg * kDecRows);
+    for (int r = 2 * warp; r < 2 * warp + 2; ++r) {
+      const int row = cur.rg * kDecRows + r;
+      const int64_t tok = (int64_t)cur.s.q0 + row / G;
+      const int hq = cur.h * G + row % G;
+      const bool ok = r < rows && tok >= 0 && tok < a.total_q;
+      constexpr int N = D / 32;
+      float q[N], mx = 0.f;
+      // lane l holds channels N l .. N l + N - 1
 #pragma unroll
-    for (int k = 0; k < N; ++k) o[k] = fmaf(sv, byte_value(vb[(32 * k + lane) * g.sub + tb], g.code), o[k] * al);
-    l = l * al + p;
-    m = mn;
+      for (int k = 0; k < N; ++k) {
+        q[k] = ok ? load_f(a.Q, tok * a.q_stride + (int64_t)hq * D + N * lane + k, g.dtype) : 0.f;
+        const float t = fabsf(q[k]);
+        mx = fmaxf(mx, t <= 3.402823466e38f ? t : 0.f);
+      }
+      mx = warp_max(mx);
+      int e = mx > 0.f ? 141 - (int)(__float_as_uint(mx) >> 23) : 0;       // 2^e mx in [2^14, 2^15)
+      e = min(e, 120);
+      const float up = __int_as_float((127 + e) << 23);
+      __half* A = reinterpret_cast<__half*>(s_q);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float v = q[k] * up;
+        const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
+        // channel 64 j + 16 c' + 4 w + b is k-step 4 j + w, lane (r, c'), register 2 (b / 2), half b mod 2
+        const int ch = N * lane + k;
+        const int ks = 4 * (ch >> 6) + ((ch >> 2) & 3), cc = (ch >> 4) & 3, b = ch & 3;
+        __half* f = A + ((ks * 32 + 4 * r + cc) * 4 + 2 * (b >> 1)) * 2 + (b & 1);
+        f[0] = hi;
+        f[2] = lo;                                                       // the next register: row r + 8
+      }
+      if (lane == 0) {
+        s_fr[r] = ok ? a.scale * kLog2e * __int_as_float((127 - e) << 23) : 0.f;
+        s_vis[r] = ok ? visible(cur.s, row / G, a.causal) : 0;
+      }
+    }
+    __syncthreads();
+    const float fr = s_fr[gi];
+    const int vis = s_vis[gi];
+    const int uvis = group_visible<kDecRows>(cur.s, G, cur.rg, a.causal);
+    float m = -INFINITY, l = 0.f;
+    float o[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = 0.f;
+
+    for (int64_t xt = x + ((warp - x) & (kDecWarps - 1)); xt < xe && uvis > 0; xt += kDecWarps) {
+      // ---- scores
+      wait_stage();
+      const unsigned char* kb = ring + cst * STB + (16 * (gi >> 1)) / SUB * SS + ((16 * (gi >> 1)) % SUB + (gi & 1)) * D + 16 * c;
+      float sc[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        uint4 A[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) A[w] = s_q[(4 * j + w) * 32 + lane];
+        const int jo = D == 64 ? 0 : (j ^ (gi & 1)) * 64;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 kw = *reinterpret_cast<const uint4*>(kb + 2 * i * D + jo);
+          uint32_t b0, b1;
+          expand4<CODE>(kw.x, b0, b1);
+          hmma16816(sc[i], A[0].x, A[0].y, A[0].z, A[0].w, b0, b1);
+          expand4<CODE>(kw.y, b0, b1);
+          hmma16816(sc[i], A[1].x, A[1].y, A[1].z, A[1].w, b0, b1);
+          expand4<CODE>(kw.z, b0, b1);
+          hmma16816(sc[i], A[2].x, A[2].y, A[2].z, A[2].w, b0, b1);
+          expand4<CODE>(kw.w, b0, b1);
+          hmma16816(sc[i], A[3].x, A[3].y, A[3].z, A[3].w, b0, b1);
+        }
+      }
+      const float f = fr * *reinterpret_cast<const float*>(ring + cst * STB + 16 * c / SUB * SS + SUB * D);
+      __syncwarp();
+      next_stage();
+      refill();
+      // ---- softmax over this lane's tokens 16 c + 2 i + {0, 1} of row gi
+      const int t0 = (int)(xt - cur.u0) * kTile + 16 * c;
+      float p[8][2], mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float s = (sc[i][e] + sc[i][e + 2]) * f;
+          p[i][e] = t0 + 2 * i + e < vis ? s : -INFINITY;
+          mx = fmaxf(mx, p[i][e]);
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
+      const float alpha = ex2(m - mu);                 // m = -inf: 0
+      m = mn;
+      float ls = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          p[i][e] = ex2(p[i][e] - mu);
+          ls += p[i][e];
+        }
+      l = l * alpha + ls;
+      // ---- P V: p times its page's scale against the tile's largest, split into two halves
+      wait_stage();
+      const float sv = *reinterpret_cast<const float*>(ring + cst * STB + 16 * c / SUB * SS + SUB * D);
+      float st = sv;
+      if constexpr (NSUB > 1) {
+        st = fmaxf(st, __shfl_xor_sync(0xffffffffu, st, 1));
+        st = fmaxf(st, __shfl_xor_sync(0xffffffffu, st, 2));
+      }
+      const float up = NSUB > 1 ? (st > 0.f ? __fdividef(sv, st) * kUp : 0.f) : kUp;
+      uint32_t ph[8], pl[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v0 = p[i][0] * up, v1 = p[i][1] * up;
+        const __half2 hi = __floats2half2_rn(v0, v1);
+        const float2 back = __half22float2(hi);
+        ph[i] = *reinterpret_cast<const uint32_t*>(&hi);
+        pl[i] = pack_half(v0 - back.x, v1 - back.y);
+      }
+      const float so = st * (1.f / kUp);
+      const unsigned char* vb = ring + cst * STB + 16 * c / SUB * SS + 16 * c % SUB + gi * SUB;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 vw = *reinterpret_cast<const uint4*>(vb + n * 8 * SUB);
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t b0, b1;
+        expand4<CODE>(vw.x, b0, b1);
+        hmma16816(acc, ph[0], pl[0], ph[1], pl[1], b0, b1);
+        expand4<CODE>(vw.y, b0, b1);
+        hmma16816(acc, ph[2], pl[2], ph[3], pl[3], b0, b1);
+        expand4<CODE>(vw.z, b0, b1);
+        hmma16816(acc, ph[4], pl[4], ph[5], pl[5], b0, b1);
+        expand4<CODE>(vw.w, b0, b1);
+        hmma16816(acc, ph[6], pl[6], ph[7], pl[7], b0, b1);
+        o[n][0] = fmaf(so, acc[0] + acc[2], o[n][0] * alpha);
+        o[n][1] = fmaf(so, acc[1] + acc[3], o[n][1] * alpha);
+      }
+      __syncwarp();
+      next_stage();
+      refill();
+    }
+
+    // ---- the warps' (m, l, o) into warp 0, in two rounds
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (c == 0) s_ml[warp][gi] = make_float2(m, l);
+    __syncthreads();
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, s_ml[w][gi].x);
+    const float Mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) L += s_ml[w][gi].y * ex2(s_ml[w][gi].x - Mu);
+    const float mine = ex2(m - Mu);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      o[i][0] *= mine;
+      o[i][1] *= mine;
+    }
+    // a lane's pairs, lane after lane: no bank conflicts
+    float2* so2 = reinterpret_cast<float2*>(s_o);
+    if (warp >= 2)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) so2[((warp - 2) * NT + i) * 32 + lane] = make_float2(o[i][0], o[i][1]);
+    __syncthreads();
+    if (warp < 2)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const float2 v = so2[(warp * NT + i) * 32 + lane];
+        o[i][0] += v.x;
+        o[i][1] += v.y;
+      }
+    __syncthreads();
+    if (warp == 1)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) so2[i * 32 + lane] = make_float2(o[i][0], o[i][1]);
+    __syncthreads();
+    const bool whole = x == cur.u0 && xe == ue;
+    const int64_t otok = (int64_t)cur.s.q0 + (cur.rg * kDecRows + gi) / G;
+    const int ohq = cur.h * G + (cur.rg * kDecRows + gi) % G;
+    if (warp == 0) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const float2 v = so2[i * 32 + lane];
+        o[i][0] += v.x;
+        o[i][1] += v.y;
+      }
+      if (whole) {
+        if (gi < rows && otok >= 0 && otok < a.total_q) {
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          const int64_t at = (otok * a.Hq + ohq) * D;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            store_f(a.out, at + 8 * i + 2 * c, g.dtype, L > 0.f ? o[i][0] * inv : 0.f);
+            store_f(a.out, at + 8 * i + 2 * c + 1, g.dtype, L > 0.f ? o[i][1] * inv : 0.f);
+          }
+          if (a.lse && c == 0) a.lse[otok * a.Hq + ohq] = L > 0.f ? (M + log2f(L)) * (1.f / kLog2e) : -INFINITY;
+        }
+      } else {
+        const int slot = 2 * cta + (x == cur.u0 ? 1 : 0);
+        float* po = ws.o + ((int64_t)slot * kDecRows + gi) * D;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          *reinterpret_cast<float2*>(po + 8 * i + 2 * c) = make_float2(o[i][0], o[i][1]);
+        if (c == 0) ws.ml[slot * kDecRows + gi] = make_float2(M, L);
+        __threadfence();
+      }
+    }
+    if (!whole) {
+      // the CTA that finishes its part of the unit last joins the parts, in their order
+      const int c0 = share_owner(W, C, cur.u0), c1 = share_owner(W, C, ue - 1);
+      __syncthreads();
+      if (tid == 0) {
+        __threadfence();
+        s_last = atomicInc(reinterpret_cast<unsigned*>(&ws.count[c0]), (unsigned)(c1 - c0)) == (unsigned)(c1 - c0);
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_last) {
+        // 16 threads per row, each D / 16 channels
+        const int r = tid >> 4, k = tid & 15;
+        constexpr int CH = D / 16;
+        auto slot_of = [&](int p) { return p == c0 ? 2 * p + 1 : 2 * p; };
+        float Ma = -INFINITY;
+        for (int p = c0; p <= c1; ++p) Ma = fmaxf(Ma, __ldcg(&ws.ml[slot_of(p) * kDecRows + r]).x);
+        const float Mb = Ma == -INFINITY ? 0.f : Ma;
+        float La = 0.f, oo[CH];
+#pragma unroll
+        for (int q = 0; q < CH; ++q) oo[q] = 0.f;
+        for (int p = c0; p <= c1; ++p) {
+          const float2 v = __ldcg(&ws.ml[slot_of(p) * kDecRows + r]);
+          const float wt = ex2(v.x - Mb);
+          La += v.y * wt;
+          const float4* src = reinterpret_cast<const float4*>(ws.o + ((int64_t)slot_of(p) * kDecRows + r) * D) + k;
+#pragma unroll
+          for (int q = 0; q < CH / 4; ++q) {
+            const float4 t = __ldcg(src + 16 * q);
+            oo[4 * q] = fmaf(t.x, wt, oo[4 * q]);
+            oo[4 * q + 1] = fmaf(t.y, wt, oo[4 * q + 1]);
+            oo[4 * q + 2] = fmaf(t.z, wt, oo[4 * q + 2]);
+            oo[4 * q + 3] = fmaf(t.w, wt, oo[4 * q + 3]);
+          }
+        }
+        const int row = cur.rg * kDecRows + r;
+        const int64_t tok = (int64_t)cur.s.q0 + row / G;
+        const int hq = cur.h * G + row % G;
+        if (r < rows && tok >= 0 && tok < a.total_q) {
+          const float inv = La > 0.f ? 1.f / La : 0.f;
+#pragma unroll
+          for (int q = 0; q < CH; ++q)
+            store_f(a.out, (tok * a.Hq + hq) * D + 64 * (q >> 2) + 4 * k + (q & 3), g.dtype, La > 0.f ? oo[q] * inv : 0.f);
+          if (a.lse && k == 0) a.lse[tok * a.Hq + hq] = La > 0.f ? (Ma + log2f(La)) * (1.f / kLog2e) : -INFINITY;
+        }
+      }
+    }
+    x = xe;
+    if (x < x1) next_unit<kDecRows, kTile>(g, a, G, cur);
   }
-#pragma unroll
-  for (int k = 0; k < N; ++k) store_f(a.out, w * D + 32 * k + lane, g.dtype, l > 0.f ? o[k] / l : 0.f);
-  if (a.lse && lane == 0) a.lse[w] = l > 0.f ? m + logf(l) : -INFINITY;
+  if (s_abort) {
+    // a wait gave up: let the copies in flight land before the shared memory is given back
+    for (int s = 0; s < NST; ++s) (void)mbar_wait(&s_full[warp][s], cph);
+  }
+}
+
+template <int D, int SUB, int CODE>
+cudaError_t decode_t(const PGeom& g, const PagedAttn& a, cudaStream_t s) {
+  constexpr size_t smem = dec_smem<D, SUB>();
+  static_assert(smem <= (DecCfg<D>::kCtas == 1 ? 226u : 113u) * 1024, "resident CTAs");
+  cudaError_t e = cudaFuncSetAttribute(k_paged_decode<D, SUB, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_paged_decode<D, SUB, CODE>, dim3(148 * DecCfg<D>::kCtas), dim3(kDecThreads), smem, s, g, a);
+}
+
+template <int D, int SUB>
+cudaError_t decode_c(const PGeom& g, const PagedAttn& a, cudaStream_t s) {
+  return g.code == TQ_CODE_INT8 ? decode_t<D, SUB, TQ_CODE_INT8>(g, a, s) : decode_t<D, SUB, TQ_CODE_E4M3>(g, a, s);
+}
+
+template <int D>
+cudaError_t decode_d(const PGeom& g, const PagedAttn& a, cudaStream_t s) {
+  if (g.sub == 16) return decode_c<D, 16>(g, a, s);
+  if (g.sub == 32) return decode_c<D, 32>(g, a, s);
+  return decode_c<D, 64>(g, a, s);
 }
 
 }  // namespace
 
-size_t paged_attn_ws_bytes(int d) { return kWsHeader; }
+size_t paged_attn_ws_bytes(int d) {
+  return kWsHeader + (size_t)2 * kMaxCtas * kDecRows * (8 + 4 * (size_t)d);
+}
 cudaError_t paged_launch_ws_init(void* ws, cudaStream_t s) {
   return launch_pdl(k_paged_ws_init, dim3(1), dim3(256), 0, s, static_cast<uint32_t*>(ws));
 }
 
 cudaError_t paged_launch_attention(const PGeom& g, const PagedAttn& a, cudaStream_t s) {
-  const dim3 grid((unsigned)((a.total_q * a.Hq + 3) / 4));
-  if (g.d == 64) return launch_pdl(k_paged_attn_plain<64>, grid, dim3(128), 0, s, g, a);
-  if (g.d == 128) return launch_pdl(k_paged_attn_plain<128>, grid, dim3(128), 0, s, g, a);
-  return launch_pdl(k_paged_attn_plain<256>, grid, dim3(128), 0, s, g, a);
+  if (g.d == 64) return decode_d<64>(g, a, s);
+  if (g.d == 128) return decode_d<128>(g, a, s);
+  return decode_d<256>(g, a, s);
 }
 
 TQ_BOUNDS_READER(bounds_flag_paged_attn)

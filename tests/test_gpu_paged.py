@@ -6,7 +6,12 @@ Attention: a logit is a sum of d products held in fp32, off by at most (d + 8) 2
 scale * sum |q k| (`reach`); a weight is then off by twice that relatively, plus the exponential
 and the sums (2^-19 together: 2 ulp of exp2, the running sums, q and p split into two halves of
 11 bits), or plus 2^-11 where p is rounded to one half (chunks of bf16 / f16).  The output is off by that
-times sum p |v| (`mass`), plus its own rounding."""
+times sum p |v| (`mass`), plus its own rounding.
+Halves also have a smallest step, 2^-24, so what is held of a tiny p is off absolutely: p (at most 1
+against the running maximum, times its page's value scale over the largest one of the tile, at most
+1) is held times 2^15, the last rounding is off by at most 2^-25, so p by 2^-40, times a code times
+the tile's largest scale, at most max |v|.  Over the visible tokens that is 2^-40 n max |v| (`floor`): later
+rescaling only shrinks it, and the sum it is divided by is at least 1."""
 import math
 
 import numpy as np
@@ -96,7 +101,8 @@ def check_attention(c, m, Q, rows, counts, causal, dtype, scale=None, single_p=F
         k, v = m.values(s, layer) if ok else (np.zeros((0, m.Hkv, d)),) * 2
         want, wl, mass, reach = op.attention(q64[at:at + n], k, v, causal, sc)
         ew = 2 * (d + 8) * 2.0 ** -24 * reach + 2.0 ** -19 + (2.0 ** -11 if single_p else 0.0)
-        tol = ew[..., None] * mass + HALF[dtype] * (np.abs(want) + ew[..., None] * mass) + TINY[dtype]
+        floor = 2.0 ** -40 * len(v) * np.abs(v).max() if len(v) else 0.0
+        tol = floor + ew[..., None] * mass + HALF[dtype] * (np.abs(want) + ew[..., None] * mass) + TINY[dtype]
         err = np.abs(host(got[at:at + n]) - want)
         assert (err <= tol).all(), (s, n, float((err / np.maximum(tol, 1e-300)).max()), float(err.max()))
         gl = got_lse[at:at + n].cpu().double().numpy()
