@@ -260,7 +260,7 @@ int tq_debug_bounds_check(void) {
                {"decode_mma", tq::bounds_flag_decode_mma}, {"decode_mma_wide", tq::bounds_flag_wide},
                {"prefill_mma", tq::bounds_flag_prefill}, {"prefill_tc", tq::bounds_flag_prefill_tc},
                {"paged_pages", tq::bounds_flag_paged_pages}, {"paged_quant", tq::bounds_flag_paged_quant},
-               {"paged_attn", tq::bounds_flag_paged_attn}};
+               {"paged_attn", tq::bounds_flag_paged_attn}, {"paged_chunk", tq::bounds_flag_paged_chunk}};
   int first = 0;
   const char* where = "";
   for (const auto& f : files) {

@@ -115,12 +115,16 @@ struct PagedAttn {
   void* ws;
 };
 size_t paged_attn_ws_bytes(int d);
+// many query rows (paged_chunk.cu)
+size_t paged_chunk_ws_bytes(int d);
+cudaError_t paged_launch_chunk(const PGeom& g, const PagedAttn& a, cudaStream_t s);
 cudaError_t paged_launch_ws_init(void* ws, cudaStream_t s);
 cudaError_t paged_launch_attention(const PGeom& g, const PagedAttn& a, cudaStream_t s);
 
 int bounds_flag_paged_pages();
 int bounds_flag_paged_quant();
 int bounds_flag_paged_attn();
+int bounds_flag_paged_chunk();
 
 // Shared with abi.cu: success (clears the thread's message), the fault injector.
 int clear_error();
