@@ -6,10 +6,11 @@
 //   S_w = Q_w K^T       A = Q_w (128 x D, shared memory), B = K (T x D), fp32 in tensor memory
 //   P_w = 2^(f S_w + log2 s_v - M)      a thread per row, f16 back into tensor memory over S_w
 //   O_w += P_w V        A = P_w (tensor memory), B = V (D x T, shared memory)
-// Four kinds of warps: one warpgroup per row block w (softmax), three converter warps that read
-// the next tile's codes into registers while they expand the last one's into the f16 operands,
-// and one warp whose first thread issues the products.  The products of one row block run while
-// the other's softmax does; with MT = 1 two S buffers take their place.
+// A warpgroup per row block runs its softmax, four converter warps read the next tile's codes
+// into registers while they expand the last one's into the f16 operands, and one warp issues the
+// products.  The products of one row block run while the other's softmax does; with MT = 1 two S
+// buffers take their place.  The roles meet at mbarriers only, so that converters run ahead into the
+// next unit while the softmax warps finish the last.
 //
 // The scales enter exactly and at no cost per element: a page's key scale multiplies the row's
 // factor f (one per 16 tokens), its value scale is added to the exponent, so that O sums code
@@ -27,7 +28,7 @@ namespace {
 using namespace paged;
 
 constexpr int kChunkCtas = 148;
-constexpr int kConv = 3;                   // converter warps; the products' warp completes their warpgroup
+constexpr int kConv = 4;                   // converter warps
 constexpr float kNone = -1e30f;            // reference of a row that has seen no token
 constexpr float kBias = 11.f;              // p is held times 2^11
 constexpr float kSlack = 4.f;
@@ -38,24 +39,65 @@ template <int D>
 __host__ __device__ constexpr int chunk_max_mt() { return D == 256 ? 1 : 2; }
 template <int D, int MT>
 __host__ __device__ constexpr size_t chunk_smem() {
-  return (size_t)MT * 128 * D * 2 + 4 * (size_t)chunk_tokens<D>() * D * 2;
+  return 1024 + (size_t)MT * 128 * D * 2 + 4 * (size_t)chunk_tokens<D>() * D * 2;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, f16 operands, issued by one thread.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// Operands lie in shared memory K-major in the 128-byte swizzle: slabs of 64 f16 along K, a row
+// of a slab 128 bytes, its 16-byte piece c at place c ^ (row mod 8); 8 rows are 1024 bytes.
+// (The plain core-matrix layout took 190 cycles a 128 x 128 x 16 product here.)
+// Byte offset of 16-byte piece c (along all of K) of `row` in an operand of ROWS rows.
+template <int ROWS>
+__device__ __forceinline__ int sw_off(int row, int c) {
+  return (c >> 3) * (ROWS * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+// Descriptor of such an operand at shared address `at` (1024-byte aligned), and what k-step k (16
+// f16) adds to it (the start address is its low field, in units of 16 bytes).
+__device__ __forceinline__ uint64_t sw_desc(uint32_t at) {
+  return (uint64_t)((at >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+template <int ROWS>
+__device__ __forceinline__ constexpr int sw_step(int k) {
+  return (k >> 2) * (ROWS * 8) + (k & 3) * 2;
+}
+
+// The products' warp runs its loop with all lanes, so that descriptors and addresses stay in uniform
+// registers (in a branch of one thread each product took 200 cycles to issue); one elected lane, always
+// the same, issues each instruction.
+// D[tmem] (+)= A[smem] * B[smem]^T, f16 operands.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on the mbarrier when every product issued so far has completed.
+__device__ __forceinline__ void mma_commit_elected(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
 
 struct ChunkWs {
-  int* count;          // [CTAs]
+  int* count;          // [CTAs][2] finished parts of the unit that goes on after the CTA, per row block
   float* lse;          // [2 x CTAs][R] log2 of a part's weight sum (-inf: none)
-  float* o;            // [2 x CTAs][R][D] a part's output
+  float* o;            // [2 x CTAs][D / 4][R][4] a part's output
 };
 template <int D, int MT>
 __device__ __forceinline__ ChunkWs chunk_ws(void* ws) {
@@ -67,33 +109,67 @@ __device__ __forceinline__ ChunkWs chunk_ws(void* ws) {
   return w;
 }
 
-template <int D, int MT>
+template <int MT>
 struct ChunkShared {
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_ready[2], pv_done[2];
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_ready[2], pv_done[2], q_full[2];
   uint64_t scales[4];
-  int64_t sum[4 * MT + 4];
+  int64_t sum[4 * MT + 8];
   float sk[4][8], lv[4][8];                // a tile's scales per 16 tokens: of the keys, log2 of the values'
+  float fr[128 * MT];                      // a row's factor on S
   Cursor cur;
   uint32_t tmem;
-  int abort, last;
+  int abort, last[2];
 };
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Wait for the tensor-memory loads of this thread, tied to the registers they fill, so that no use
+// of those is moved before it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27])
+               :
+               : "memory");
+  asm volatile("" : "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]) : : "memory");
+}
+
+// Two entries of a model type as floats, and back.
+__device__ __forceinline__ float2 unpack2(uint32_t u, bool f16) {
+  return f16 ? __half22float2(*reinterpret_cast<const __half2*>(&u))
+             : make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, bool f16) {
+  if (f16) return pack_half(a, b);
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 template <int D, int CODE, int MT>
-__global__ void __launch_bounds__(128 * MT + 128, 1) k_paged_chunk(PGeom g, PagedAttn a) {
-  constexpr int T = chunk_tokens<D>(), R = 128 * MT, NTH = R + 128;
-  constexpr int NG = T / 16;                          // 16-token groups of a tile
-  constexpr int NB = T * D / 512;                     // 8-row x 64-byte pieces of a tile's keys (values)
-  constexpr int NK = (NB + kConv - 1) / kConv;        // of them per converter warp
+__global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, PagedAttn a) {
+  constexpr int T = chunk_tokens<D>(), R = 128 * MT, NTH = R + 256;
+  constexpr int TW = T / kConv;                       // tokens of a tile a converter warp expands
+  constexpr int NK = T * D / 16 / 128;                // 16-byte pieces of a tile's keys (values) per converter lane
   constexpr uint32_t kTb = T * D * 2;                 // bytes of an f16 operand tile
   constexpr uint32_t cO = 0, cS = MT * D;             // tensor memory columns
-  extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ ChunkShared<D, MT> sh;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  __shared__ ChunkShared<MT> sh;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);       // known to be the same in all lanes
   const int wg = warp >> 2;                           // < MT: softmax of row block wg
-  const bool is_soft = wg < MT, is_mma = warp == 4 * MT + kConv, is_conv = !is_soft && !is_mma;
+  const bool is_soft = wg < MT, is_conv = wg == MT, is_mma = warp == 4 * MT + kConv;   // the other three warps rest
   const uint32_t sQ = smem_u32(smem), sK = sQ + R * D * 2, sV = sK + 2 * kTb;
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.scales[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.scales[i], kConv);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.k_full[i], kConv);
       mbar_init(&sh.k_free[i], 1);
@@ -102,6 +178,7 @@ __global__ void __launch_bounds__(128 * MT + 128, 1) k_paged_chunk(PGeom g, Page
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_ready[i], 4);
       mbar_init(&sh.pv_done[i], 1);
+      mbar_init(&sh.q_full[i], 4);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sh.abort = 0;
@@ -133,7 +210,6 @@ __global__ void __launch_bounds__(128 * MT + 128, 1) k_paged_chunk(PGeom g, Page
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem;
   Cursor cur = sh.cur;
-  const ChunkWs ws = chunk_ws<D, MT>(a.ws);
   auto wait = [&](uint64_t* bar, int index) {         // completion `index` (0, 1, ...) of a barrier
     if (*static_cast<volatile int*>(&sh.abort)) return;
     if (!mbar_wait_timed(bar, (uint32_t)(index & 1))) {
@@ -141,245 +217,274 @@ __global__ void __launch_bounds__(128 * MT + 128, 1) k_paged_chunk(PGeom g, Page
       atomicOr(&g.state->status, kPagedWait);
     }
   };
-
-  int n0 = 0;                                         // tiles of this CTA before the segment
-  int64_t x = x0;
-  while (x < x1) {
-    const int64_t ue = cur.u0 + cur.nt, xe = min(x1, ue);
-    const int uvis = group_visible<R>(cur.s, G, cur.rg, a.causal);
-    const int nt = uvis > 0 ? (int)(xe - x) : 0;      // tiles of the segment
-    const int tok0 = (int)(x - cur.u0) * T;           // its first token
-    const int rows = (int)min((int64_t)R, (int64_t)cur.s.nq * G - (int64_t)cur.rg * R);
-    float fr = 0.f, M = kNone, l = 0.f, lvr = 0.f;
-    int vis = 0;
-    __syncthreads();                                  // the last segment's operands are free
-
-    if (is_soft) {
-      // ---- this thread's query row into the A operand
-      const int r = tid, row = cur.rg * R + r;
-      const int64_t tok = (int64_t)cur.s.q0 + row / G;
-      const bool ok = r < rows && tok >= 0 && tok < a.total_q;
-      if (ok) vis = visible(cur.s, row / G, a.causal);
-      uint4 q[D / 8];
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + tok * a.q_stride +
-                                                        (int64_t)(cur.h * G + row % G) * D);
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) q[k] = ok ? src[k] : make_uint4(0, 0, 0, 0);
-      auto both = [&](uint32_t u) {
-        return g.dtype == TQ_F16 ? __half22float2(*reinterpret_cast<const __half2*>(&u))
-                                 : make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-      };
-      float mx = 0.f;
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = both(w[i]);
-          const float t0 = fabsf(v.x), t1 = fabsf(v.y);
-          mx = fmaxf(mx, t0 <= 3.402823466e38f ? t0 : 0.f);
-          mx = fmaxf(mx, t1 <= 3.402823466e38f ? t1 : 0.f);
-        }
-      }
-      // the largest entry of the row into [2^14, 2^15); a negative scale turns the row's sign
-      int e = mx > 0.f ? 141 - (int)(__float_as_uint(mx) >> 23) : 0;
-      e = min(e, 120);
-      const float up = copysignf(__int_as_float((127 + e) << 23), a.scale);
-      fr = ok ? fabsf(a.scale) * kLog2e * __int_as_float((127 - e) << 23) : 0.f;
-      unsigned char* Q = smem + (size_t)(r >> 7) * 128 * D * 2;
-      const int rr = r & 127;
-#pragma unroll
-      for (int k = 0; k < D / 8; ++k) {
-        const uint32_t w[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = both(w[i]);
-          o[i] = pack_half(v.x * up, v.y * up);
-        }
-        *reinterpret_cast<uint4*>(Q + ((rr >> 3) * (D / 8) + k) * 128 + (rr & 7) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-      tc::fence_async_shared();
+  // Each role walks the CTA's units by itself: f(first tile of the segment in its unit, tiles of the
+  // segment (0 for a unit that sees nothing), tiles of the CTA before it, segments with tiles before it).
+  auto walk = [&](auto f) {
+    int64_t x = x0;
+    int n0 = 0, seg = 0;
+    while (x < x1) {
+      const int64_t xe = min(x1, cur.u0 + cur.nt);
+      const int nt = group_visible<R>(cur.s, G, cur.rg, a.causal) > 0 ? (int)(xe - x) : 0;
+      f(x, xe, nt, n0, seg);
+      n0 += nt;
+      seg += nt > 0;
+      x = xe;
+      if (x < x1) next_unit<R, T>(g, a, G, cur);
     }
-    __syncthreads();
+  };
 
-    if (is_conv) {
-      // ================================================= converters
-      const int cw = warp & 3;
-      const int lsub = 31 - __clz(g.sub);
-      const int64_t vofs = (int64_t)g.Hkv * g.hb;
-      const int last = cur.s.len - 1;
+  if (is_conv) {
+    // =================================================================== converters
+    // Warp cw expands tokens cw TW ... of the tile, in halves of 16 that lie in one sub-block.  A warp
+    // instruction takes 8 rows of 4 pieces (keys) or 8 channels of each half (values), so that its 16-byte
+    // stores hit all banks; rows are 128 bytes of the swizzled operand.
+    constexpr int NH = TW / 16;
+    const int cw = warp & 3, l7 = lane & 7, l3 = lane >> 3, par = lane & 1;
+    const int lsub = 31 - __clz(g.sub);
+    const int64_t vofs = (int64_t)g.Hkv * g.hb;
+    const int ko[2] = {D == 64 ? l7 * D + 16 * l3 : l7 * D + 16 * l3 + 64 * par,
+                       D == 64 ? 0 : l7 * D + 16 * l3 + 64 * (1 - par)};
+    const int vh = NH == 2 ? l3 & 1 : 0;              // the half and the channel of this lane's value pieces
+    const int vch = NH == 2 ? (lane >> 4) * 8 + l7 : lane;
+    constexpr int VSTEP = NH == 2 ? 16 : 32;
+    const int pc = 2 * (cw * NH + vh);                // their piece along T
+    const int kd0 = (cw * TW + l7) * 128 + (((2 * l3) ^ l7) << 4), kd1 = (cw * TW + l7) * 128 + (((2 * l3 + 1) ^ l7) << 4);
+    const int vd0 = sw_off<D>(vch, pc), vd1 = sw_off<D>(vch, pc + 1);
+    auto put = [&](unsigned char* to, unsigned char* to2, const uint4& v) {        // 16 codes -> two pieces of a row
+      uint32_t o[8];
+      expand4<CODE>(v.x, o[0], o[1]);
+      expand4<CODE>(v.y, o[2], o[3]);
+      expand4<CODE>(v.z, o[4], o[5]);
+      expand4<CODE>(v.w, o[6], o[7]);
+      *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(to2) = make_uint4(o[4], o[5], o[6], o[7]);
+    };
+    walk([&](int64_t x, int64_t, int nt, int n0, int) {
+      if (nt == 0) return;
+      const int tok0 = (int)(x - cur.u0) * T + cw * TW, last = cur.s.len - 1;
+      const int* table = g.table + (int64_t)cur.s.slot * g.max_pages;
       uint4 kr[NK], vr[NK];
-      const uint8_t* ptr = nullptr;                   // lane k: key sub-block k of the tile in hand
+      int pid[NH], off[NH];                           // page and token offset in it of each half, a tile ahead
+      const uint8_t* kp[NH];
       float sk = 0.f, sv = 0.f;
-      int pid = 0, psub = 0;
-      auto look = [&](int t) {                        // lane k: page of sub-block k of tile t
-        const int tk = min(tok0 + t * T + (lane << lsub), last);     // past the end: the last one, masked
-        pid = lane < (T >> lsub) ? g.table[(int64_t)cur.s.slot * g.max_pages + tk / g.page] : 0;
-        psub = (tk % g.page) >> lsub;
-      };
-      auto aim = [&]() {
-        if ((unsigned)pid >= (unsigned)g.pages) {
-          atomicOr(&g.state->status, kPagedBadPage);
-          pid = 0;
+      auto look = [&](int t) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          // past the end: the last sub-block's, masked but finite
+          const int tk = min(tok0 + t * T + 16 * h, last & ~15);
+          pid[h] = table[tk / g.page];
+          off[h] = tk % g.page;
         }
-        ptr = paged_block(g, a.layer, pid, 0, cur.h, psub);
-      };
-      auto sub_ptr = [&](int i) {                     // sub-block i's pointer, from lane i
-        return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(ptr), i));
       };
       auto load_k = [&]() {
 #pragma unroll
-        for (int it = 0; it < NK; ++it) {
-          const int b = it * kConv + cw, row = (b / (D / 64)) * 8 + (lane & 7), ch = (b % (D / 64)) * 4 + (lane >> 3);
-          if (b >= NB) break;
-          const uint8_t* p = sub_ptr(row >> lsub) + paged_k_off(D, row & (g.sub - 1), 16 * ch);
-          kr[it] = TQ_CHECKED(p, 16, g.base, g.total, 421) ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < NH; ++h) {
+          if ((unsigned)pid[h] >= (unsigned)g.pages) {
+            if (lane == 0) atomicOr(&g.state->status, kPagedBadPage);
+            pid[h] = 0;
+          }
+          kp[h] = paged_block(g, a.layer, pid[h], 0, cur.h, off[h] >> lsub);
+          off[h] &= g.sub - 1;
         }
-        const uint8_t* p = sub_ptr((16 * (lane & (NG - 1))) >> lsub);
-        sk = *reinterpret_cast<const float*>(p + g.sub * D);
-        sv = *reinterpret_cast<const float*>(p + vofs + g.sub * D);
-      };
-      auto load_v = [&]() {
 #pragma unroll
         for (int it = 0; it < NK; ++it) {
-          const int b = it * kConv + cw, ch = (b / (T / 64)) * 8 + (lane & 7), q = (b % (T / 64)) * 4 + (lane >> 3);
-          if (b >= NB) break;
-          const uint8_t* p = sub_ptr((16 * q) >> lsub) + vofs + ((int64_t)ch << lsub) + ((16 * q) & (g.sub - 1));
-          vr[it] = TQ_CHECKED(p, 16, g.base, g.total, 422) ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+          const int cg = it % (D / 64), rg = it / (D / 64);          // 8-row group, 64-byte group
+          const uint8_t* p = kp[rg / 2] + off[rg / 2] * D + ko[cg & 1] + (cg >> 1) * 128 + (rg & 1) * 8 * D;
+          kr[it] = TQ_CHECKED(p, 16, g.base, g.total, 421) ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+        }
+        const uint8_t* tr = (NH == 2 && (lane & 1) ? kp[NH - 1] : kp[0]) + ((int64_t)D << lsub);
+        sk = *reinterpret_cast<const float*>(tr);
+        sv = *reinterpret_cast<const float*>(tr + vofs);
+      };
+      auto load_v = [&]() {
+        const uint8_t* p = (vh ? kp[NH - 1] + off[NH - 1] : kp[0] + off[0]) + vofs + (vch << lsub);
+#pragma unroll
+        for (int it = 0; it < NK; ++it) {
+          const uint8_t* q = p + ((it * VSTEP) << lsub);
+          vr[it] = TQ_CHECKED(q, 16, g.base, g.total, 422) ? *reinterpret_cast<const uint4*>(q) : make_uint4(0, 0, 0, 0);
         }
       };
-      auto put = [&](unsigned char* to, const uint4& v) {        // 16 codes -> two 16-byte pieces of a row
-        uint32_t o[8];
-        expand4<CODE>(v.x, o[0], o[1]);
-        expand4<CODE>(v.y, o[2], o[3]);
-        expand4<CODE>(v.z, o[4], o[5]);
-        expand4<CODE>(v.w, o[6], o[7]);
-        *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(to + 128) = make_uint4(o[4], o[5], o[6], o[7]);
-      };
-      if (nt > 0) {
-        look(0);
-        aim();
-        load_k();
-        load_v();
-        if (nt > 1) look(1);
-      }
+      look(0);
+      load_k();
+      load_v();
+      if (nt > 1) look(1);
       for (int t = 0; t < nt; ++t) {
         const int n = n0 + t, b2 = n & 1;
         unsigned char* K = smem + R * D * 2 + b2 * kTb;
         unsigned char* V = K + 2 * kTb;
         if (n >= 2) wait(&sh.k_free[b2], (n >> 1) - 1);
         // four sets of scales: the products of tile n - 2 are done, so the softmax of tile n - 4 is
-        if (cw == 0 && lane < NG) {
-          sh.sk[n & 3][lane] = sk;
-          sh.lv[n & 3][lane] = sv > 0.f ? __log2f(sv) : 0.f;     // a block of zeros: any scale will do
+        if (lane < NH) {
+          sh.sk[n & 3][cw * NH + lane] = sk;
+          sh.lv[n & 3][cw * NH + lane] = sv > 0.f ? __log2f(sv) : 0.f;     // a block of zeros: any scale will do
         }
         __syncwarp();
-        if (cw == 0 && lane == 0) mbar_arrive(&sh.scales[n & 3]);
+        if (lane == 0) mbar_arrive(&sh.scales[n & 3]);
 #pragma unroll
         for (int it = 0; it < NK; ++it) {
-          const int b = it * kConv + cw, rg = b / (D / 64), ch = (b % (D / 64)) * 4 + (lane >> 3);
-          if (b < NB) put(K + (rg * (D / 8) + 2 * ch) * 128 + (lane & 7) * 16, kr[it]);
+          unsigned char* to = K + (it % (D / 64)) * (T * 128) + (it / (D / 64)) * 1024;
+          put(to + kd0, to + kd1, kr[it]);
         }
         tc::fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.k_full[b2]);
         // the next tile's pages were looked up a tile ago; its keys travel while the values expand
-        if (t + 1 < nt) {
-          aim();
-          load_k();
-          if (t + 2 < nt) look(t + 2);
-        }
+        if (t + 1 < nt) load_k();
         if (n >= 2) wait(&sh.v_free[b2], (n >> 1) - 1);
 #pragma unroll
-        for (int it = 0; it < NK; ++it) {
-          const int b = it * kConv + cw, rg = b / (T / 64), q = (b % (T / 64)) * 4 + (lane >> 3);
-          if (b < NB) put(V + (rg * (T / 8) + 2 * q) * 128 + (lane & 7) * 16, vr[it]);
-        }
+        for (int it = 0; it < NK; ++it) put(V + vd0 + it * VSTEP * 128, V + vd1 + it * VSTEP * 128, vr[it]);
         tc::fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.v_full[b2]);
         if (t + 1 < nt) load_v();
+        if (t + 2 < nt) look(t + 2);
       }
-    } else if (is_mma) {
-      // ================================================= products
-      if (lane == 0 && nt > 0) {
-        constexpr uint32_t iS = tc::idesc_f16(128, T), iO = tc::idesc_f16(128, D);
-        auto qk = [&](int w, int sb, int b2) {
+    });
+  } else if (is_mma) {
+    // =================================================================== products
+    constexpr uint32_t iS = tc::idesc_f16(128, T), iO = tc::idesc_f16(128, D);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t dQ = sw_desc(__shfl_sync(0xffffffffu, sQ, 0)), dK = sw_desc(__shfl_sync(0xffffffffu, sK, 0)),
+                   dV = sw_desc(__shfl_sync(0xffffffffu, sV, 0));
+    auto qk = [&](int w, int sb, int b2) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc::mma_f16(tmem + cS + sb * T, tc::smem_desc_sbo(sQ + w * 128 * D * 2 + 256 * k, 16 * D),
-                        tc::smem_desc_sbo(sK + b2 * kTb + 256 * k, 16 * D), iS, k > 0);
-        };
-        auto pv = [&](int w, int sb, int b2, bool first) {
+      for (int k = 0; k < D / 16; ++k)
+        mma_ss(tm + cS + sb * T, dQ + (uint64_t)(w * (128 * D * 2 / 16) + sw_step<128>(k)),
+               dK + (uint64_t)(b2 * (kTb / 16) + sw_step<T>(k)), iS, k > 0);
+    };
+    auto pv = [&](int w, int sb, int b2, bool first) {
 #pragma unroll
-          for (int k = 0; k < T / 16; ++k)
-            mma_f16_ts(tmem + cO + w * D, tmem + cS + sb * T + 8 * k,
-                       tc::smem_desc_sbo(sV + b2 * kTb + 256 * k, 16 * T), iO, !(first && k == 0));
-        };
-        if constexpr (MT == 2) {
-          wait(&sh.k_full[n0 & 1], n0 >> 1);
+      for (int k = 0; k < T / 16; ++k)
+        mma_ts(tm + cO + w * D, tm + cS + sb * T + 8 * k, dV + (uint64_t)(b2 * (kTb / 16) + sw_step<D>(k)), iO,
+               !(first && k == 0));
+    };
+    walk([&](int64_t, int64_t, int nt_, int n0_, int seg_) {
+      const int nt = __shfl_sync(0xffffffffu, nt_, 0), n0 = __shfl_sync(0xffffffffu, n0_, 0),
+                seg = __shfl_sync(0xffffffffu, seg_, 0);
+      if (nt == 0) return;
+      // q_full: the row block's queries are in place, and its last unit's O has been read
+      if constexpr (MT == 2) {
+        wait(&sh.k_full[n0 & 1], n0 >> 1);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          wait(&sh.q_full[w], seg);
           tc::fence_after_sync();
-          qk(0, 0, n0 & 1);
-          tc::mma_commit(smem_u32(&sh.s_full[0]));
-          qk(1, 1, n0 & 1);
-          tc::mma_commit(smem_u32(&sh.s_full[1]));
-          tc::mma_commit(smem_u32(&sh.k_free[n0 & 1]));
-          for (int t = 0; t < nt; ++t) {
-            const int n = n0 + t, b2 = n & 1, m = n + 1;
-            wait(&sh.v_full[b2], n >> 1);
+          qk(w, w, n0 & 1);
+          mma_commit_elected(&sh.s_full[w]);
+        }
+        mma_commit_elected(&sh.k_free[n0 & 1]);
+        for (int t = 0; t < nt; ++t) {
+          const int n = n0 + t, b2 = n & 1, m = n + 1;
+          wait(&sh.v_full[b2], n >> 1);
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              wait(&sh.p_ready[w], n);
-              tc::fence_after_sync();
-              pv(w, w, b2, t == 0);
-              tc::mma_commit(smem_u32(&sh.pv_done[w]));
-              if (w == 1) tc::mma_commit(smem_u32(&sh.v_free[b2]));
-              if (t + 1 < nt) {
-                if (w == 0) wait(&sh.k_full[m & 1], m >> 1);
-                wait(&sh.pv_done[w], n);              // P_w lies over S_w
-                tc::fence_after_sync();
-                qk(w, w, m & 1);
-                tc::mma_commit(smem_u32(&sh.s_full[w]));
-                if (w == 1) tc::mma_commit(smem_u32(&sh.k_free[m & 1]));
-              }
-            }
-          }
-        } else {
-          for (int t = -1; t < nt; ++t) {
-            const int n = n0 + t, m = n + 1;
+          for (int w = 0; w < 2; ++w) {
+            wait(&sh.p_ready[w], n);
+            tc::fence_after_sync();
+            pv(w, w, b2, t == 0);
+            mma_commit_elected(&sh.pv_done[w]);
+            if (w == 1) mma_commit_elected(&sh.v_free[b2]);
             if (t + 1 < nt) {
-              wait(&sh.k_full[m & 1], m >> 1);
-              if (t >= 1) wait(&sh.pv_done[m & 1], (n - 1) >> 1);      // its P lies over this S buffer
+              if (w == 0) wait(&sh.k_full[m & 1], m >> 1);
+              wait(&sh.pv_done[w], n);              // P_w lies over S_w
               tc::fence_after_sync();
-              qk(0, m & 1, m & 1);
-              tc::mma_commit(smem_u32(&sh.s_full[m & 1]));
-              tc::mma_commit(smem_u32(&sh.k_free[m & 1]));
-            }
-            if (t >= 0) {
-              wait(&sh.v_full[n & 1], n >> 1);
-              wait(&sh.p_ready[n & 1], n >> 1);
-              tc::fence_after_sync();
-              pv(0, n & 1, n & 1, t == 0);
-              tc::mma_commit(smem_u32(&sh.pv_done[n & 1]));
-              tc::mma_commit(smem_u32(&sh.v_free[n & 1]));
+              qk(w, w, m & 1);
+              mma_commit_elected(&sh.s_full[w]);
+              if (w == 1) mma_commit_elected(&sh.k_free[m & 1]);
             }
           }
         }
+      } else {
+        wait(&sh.q_full[0], seg);
+        for (int t = -1; t < nt; ++t) {
+          const int n = n0 + t, m = n + 1;
+          if (t + 1 < nt) {
+            wait(&sh.k_full[m & 1], m >> 1);
+            if (t >= 1) wait(&sh.pv_done[m & 1], (n - 1) >> 1);      // its P lies over this S buffer
+            tc::fence_after_sync();
+            qk(0, m & 1, m & 1);
+            mma_commit_elected(&sh.s_full[m & 1]);
+            mma_commit_elected(&sh.k_free[m & 1]);
+          }
+          if (t >= 0) {
+            wait(&sh.v_full[n & 1], n >> 1);
+            wait(&sh.p_ready[n & 1], n >> 1);
+            tc::fence_after_sync();
+            pv(0, n & 1, n & 1, t == 0);
+            mma_commit_elected(&sh.pv_done[n & 1]);
+            mma_commit_elected(&sh.v_free[n & 1]);
+          }
+        }
       }
-      __syncwarp();
-    } else {
-      // ================================================= softmax
-      const uint32_t lrow = (uint32_t)(32 * (warp & 3)) << 16;
-      const uint32_t tO = tmem + lrow + cO + wg * D;
+    });
+  } else if (is_soft) {
+    // =================================================================== softmax
+    const uint32_t lrow = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tO = tmem + lrow + cO + wg * D;
+    const bool f16 = g.dtype == TQ_F16;
+    const int w4 = warp & 3, r = tid;                  // this thread's row of the CTA's
+    unsigned char* Q = smem + (size_t)wg * 128 * D * 2;  // the row block's operand, later its output
+    const ChunkWs ws = chunk_ws<D, MT>(a.ws);
+    // row / G for row < 2^27, G <= 8: the reciprocal's error times row stays below 1 / G
+    const uint32_t gm = (uint32_t)(0x100000000ull / (uint32_t)G) + 1u;
+    auto by_g = [&](int row) { return G == 1 ? row : (int)__umulhi((uint32_t)row, gm); };
+    // rows of D / 8 16-byte pieces: RL lanes a row, RI rows an instruction
+    constexpr int RL = D / 8, RI = 32 / RL;
+    walk([&](int64_t x, int64_t xe, int nt, int n0, int) {
+      const int64_t ue = cur.u0 + cur.nt;
+      const int tok0 = (int)(x - cur.u0) * T;          // the segment's first token
+      const int rows = (int)min((int64_t)R, (int64_t)cur.s.nq * G - (int64_t)cur.rg * R);
+      const int row0 = cur.rg * R;                     // the CTA's first row of the sequence (below 2^27)
+      // place of CTA row i's D entries in Q and out (heads of a token lie side by side); -1: none
+      auto place = [&](int i, int64_t stride) {
+        const int q = by_g(row0 + i);
+        const int64_t tok = (int64_t)cur.s.q0 + q;
+        return i < rows && tok >= 0 && tok < a.total_q ? tok * stride + (cur.h * G + row0 + i - q * G) * D : (int64_t)-1;
+      };
+      const bool ok = place(r, 0) >= 0;
+      const int vis = ok ? visible(cur.s, by_g(row0 + r), a.causal) : 0;
+      float fr = 0.f, M = kNone, l = 0.f, lvr = 0.f;
+      if (nt > 0) {
+        // ---- the warp's 32 query rows into the A operand: the largest entry of a row into [2^14,
+        // 2^15) by a power of two; a negative scale turns the row's sign
+#pragma unroll 4
+        for (int i = 0; i < 32 / RI; ++i) {
+          const int rr = 32 * w4 + i * RI + lane / RL, c = lane % RL;
+          const int64_t at = place(128 * wg + rr, a.q_stride);
+          const uint4 q = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + at)[c] : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+          float mx = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = unpack2(w[k], f16);
+            const float t0 = fabsf(v.x), t1 = fabsf(v.y);
+            mx = fmaxf(mx, fmaxf(t0 <= 3.402823466e38f ? t0 : 0.f, t1 <= 3.402823466e38f ? t1 : 0.f));
+          }
+#pragma unroll
+          for (int o = RL / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const int e = min(mx > 0.f ? 141 - (int)(__float_as_uint(mx) >> 23) : 0, 120);
+          const float up = copysignf(__int_as_float((127 + e) << 23), a.scale);
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = unpack2(w[k], f16);
+            o[k] = pack_half(v.x * up, v.y * up);
+          }
+          *reinterpret_cast<uint4*>(Q + sw_off<128>(rr, c)) = make_uint4(o[0], o[1], o[2], o[3]);
+          if (c == 0) sh.fr[128 * wg + rr] = fabsf(a.scale) * kLog2e * __int_as_float((127 - e) << 23);
+        }
+        tc::fence_async_shared();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full[wg]);
+        fr = ok ? sh.fr[r] : 0.f;
+      }
       // A parity tells a completion only from its neighbours, so every waiter has to be within one
       // of it.  MT = 2: S_w of tile n came after the products P V of n - 1.  MT = 1: after those of
       // n - 2 only, hence a barrier per buffer.
       auto pv_wait = [&](int n) {
         if (MT == 2) wait(&sh.pv_done[wg], n); else wait(&sh.pv_done[n & 1], n >> 1);
       };
-      // rows of the warp see at least wmin tokens (those in use)
+      // the rows of the warp see at least wmin tokens
       const int wmin = __reduce_min_sync(0xffffffffu, vis);
       for (int t = 0; t < nt; ++t) {
         const int n = n0 + t, sc = n & 3;
@@ -389,48 +494,33 @@ __global__ void __launch_bounds__(128 * MT + 128, 1) k_paged_chunk(PGeom g, Page
         if (MT == 2) wait(&sh.s_full[wg], n); else wait(&sh.s_full[n & 1], n >> 1);
         tc::fence_after_sync();
         if (t == 0) lvr = sh.lv[sc][0];
-        const bool masked = base + T > wmin;           // uniform in the warp
-        uint32_t pk[T / 2];
-        float zmax, ladd;
-        // exponents f S + c of the tile against M; their largest, and (EXP) p and its sum
-        auto pass = [&](auto EXP, auto MASK) {
-          zmax = -INFINITY;
-          ladd = 0.f;
+        // S in pieces of 32 columns, the next requested while one is worked on
+        auto columns = [&](auto f) {
+          uint32_t v[2][32];
+          tc::tmem_ld32(tS, v[0]);
+          tmem_wait_ld(v[0]);
 #pragma unroll
           for (int c = 0; c < T / 32; ++c) {
-            uint32_t v[32];
-            tc::tmem_ld32(tS + 32 * c, v);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float f = fr * sh.sk[sc][2 * c + h];
-              const float lv = sh.lv[sc][2 * c + h];
-              const float cst = decltype(EXP)::value ? lv - M + kBias : lv;
-              const float2 f2 = make_float2(f, f), c2 = make_float2(cst, cst);
-              float2 ls = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int col = 32 * c + 16 * h + 2 * i;
-                float2 z = fma2(make_float2(__uint_as_float(v[16 * h + 2 * i]), __uint_as_float(v[16 * h + 2 * i + 1])), f2, c2);
-                if (decltype(MASK)::value) {
-                  z.x = base + col < vis ? z.x : -INFINITY;
-                  z.y = base + col + 1 < vis ? z.y : -INFINITY;
-                }
-                zmax = fmaxf(zmax, fmaxf(z.x, z.y));
-                if (decltype(EXP)::value) {
-                  const float2 p = make_float2(ex2(z.x), ex2(z.y));
-                  ls = add2(ls, p);
-                  pk[16 * c + 8 * h + i] = pack_half(p.x, p.y);
-                }
-              }
-              if (decltype(EXP)::value) ladd = fmaf(ls.x + ls.y, ex2(lvr - lv), ladd);
-            }
+            if (c + 1 < T / 32) tc::tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
+            f(c, v[c & 1]);
+            if (c + 1 < T / 32) tmem_wait_ld(v[(c + 1) & 1]);
           }
         };
-        bool fresh = __any_sync(0xffffffffu, M == kNone && vis > base);
-        for (;;) {
-          if (fresh) {
-            if (masked) pass(std::false_type(), std::true_type()); else pass(std::false_type(), std::false_type());
+        auto both_passes = [&](auto MASK) {
+          auto hide = [&](int col, float z) { return !decltype(MASK)::value || base + col < vis ? z : -INFINITY; };
+          // the largest exponent f S + log2 s_v
+          float zmax = -INFINITY;
+          columns([&](int c, const uint32_t (&v)[32]) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float m = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) m = fmaxf(m, hide(32 * c + 16 * h + i, __uint_as_float(v[16 * h + i])));
+              const float z = fmaf(m, fr * sh.sk[sc][2 * c + h], sh.lv[sc][2 * c + h]);
+              zmax = fmaxf(zmax, m == -INFINITY ? m : z);
+            }
+          });
+          if (__any_sync(0xffffffffu, M == kNone ? zmax > -INFINITY : zmax > M + kSlack)) {
             const float Mn = M == kNone ? (zmax == -INFINITY ? kNone : zmax) : fmaxf(M, zmax);
             const float alpha = M == kNone ? 0.f : ex2(M - Mn);
             M = Mn;
@@ -442,26 +532,35 @@ __global__ void __launch_bounds__(128 * MT + 128, 1) k_paged_chunk(PGeom g, Page
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t v[32];
                 tc::tmem_ld32(tO + 32 * c, v);
-                tc::tmem_wait_ld();
+                tmem_wait_ld(v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
                 tc::tmem_st32(tO + 32 * c, v);
               }
             }
           }
-          if (masked) pass(std::true_type(), std::true_type()); else pass(std::true_type(), std::false_type());
-          if (fresh) break;
-          fresh = __any_sync(0xffffffffu, zmax > kBias + kSlack);
-          if (!fresh) break;
-        }
-        l += ladd;
+          // p and its sum; 32 columns of S give 16 of P, which lie over columns already read
+          columns([&](int c, const uint32_t (&v)[32]) {
+            uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < T / 64; ++c) {
-          uint32_t v[32];
+            for (int h = 0; h < 2; ++h) {
+              const float f = fr * sh.sk[sc][2 * c + h], lv = sh.lv[sc][2 * c + h], cst = lv - M + kBias;
+              const float2 f2 = make_float2(f, f), c2 = make_float2(cst, cst);
+              float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = pk[32 * c + i];
-          tc::tmem_st32(tS + 32 * c, v);
-        }
+              for (int i = 0; i < 8; ++i) {
+                const int col = 32 * c + 16 * h + 2 * i;
+                float2 z = fma2(make_float2(__uint_as_float(v[16 * h + 2 * i]), __uint_as_float(v[16 * h + 2 * i + 1])), f2, c2);
+                const float2 p = make_float2(ex2(hide(col, z.x)), ex2(hide(col + 1, z.y)));
+                ls = add2(ls, p);
+                pk[8 * h + i] = pack_half(p.x, p.y);
+              }
+              l = fmaf(ls.x + ls.y, ex2(lvr - lv), l);
+            }
+            tmem_st16(tS + 16 * c, pk);
+          });
+        };
+        if (base + T > wmin) both_passes(std::true_type()); else both_passes(std::false_type());
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -470,109 +569,97 @@ __global__ void __launch_bounds__(128 * MT + 128, 1) k_paged_chunk(PGeom g, Page
       }
       // ---- the row's output, or its part
       const bool whole = x == cur.u0 && xe == ue;
-      const int r = tid, row = cur.rg * R + r;
-      const int64_t tok = (int64_t)cur.s.q0 + row / G;
-      const int hq = cur.h * G + row % G;
-      const bool ok = r < rows && tok >= 0 && tok < a.total_q;
       const float inv = l > 0.f ? ex2(lvr) / l : 0.f;
       const float lse2 = l > 0.f ? log2f(l) + (M - lvr - kBias) : -INFINITY;
+      const int64_t lse_at = ((int64_t)cur.s.q0 + by_g(row0 + r)) * a.Hq + cur.h * G + row0 + r - by_g(row0 + r) * G;
       const int slot = 2 * cta + (x == cur.u0 ? 1 : 0);
       if (nt > 0) {
-        pv_wait(n0 + nt - 1);
+        pv_wait(n0 + nt - 1);                          // (and so the row block's products with Q are done)
         tc::fence_after_sync();
       }
-#pragma unroll
+      // the warp's rows from the operand's place to the output, whole rows at a time
+      auto rows_out = [&]() {
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < 32 / RI; ++i) {
+          const int rr = 32 * w4 + i * RI + lane / RL, c = lane % RL;
+          const int64_t at = place(128 * wg + rr, (int64_t)a.Hq * D);
+          const uint4 v = *reinterpret_cast<const uint4*>(Q + sw_off<128>(rr, c));
+          if (at >= 0) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at)[c] = v;
+        }
+        __syncwarp();
+      };
+      float4* part = reinterpret_cast<float4*>(ws.o + (int64_t)slot * R * D) + r;      // [D / 4][R]
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
         if (nt > 0) {
           tc::tmem_ld32(tO + 32 * c, v);
-          tc::tmem_wait_ld();
+          tmem_wait_ld(v);
         }
-        float o[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = l > 0.f ? __uint_as_float(v[i]) * inv : 0.f;
-        if (!whole) {
-          float4* po = reinterpret_cast<float4*>(ws.o + ((int64_t)slot * R + r) * D + 32 * c);
-          if (r < rows)
+        for (int i = 0; i < 4; ++i) {
+          float o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) po[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        } else if (ok) {
-          uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (tok * a.Hq + hq) * D + 32 * c);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (g.dtype == TQ_F16) {
-                w[k] = pack_half(o[8 * i + 2 * k], o[8 * i + 2 * k + 1]);
-              } else {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * i + 2 * k], o[8 * i + 2 * k + 1]);
-                w[k] = *reinterpret_cast<const uint32_t*>(&b);
-              }
-            }
-            to[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < 8; ++k) o[k] = l > 0.f ? __uint_as_float(v[8 * i + k]) * inv : 0.f;
+          if (whole) {
+            *reinterpret_cast<uint4*>(Q + sw_off<128>(r & 127, 4 * c + i)) =
+                make_uint4(pack2(o[0], o[1], f16), pack2(o[2], o[3], f16), pack2(o[4], o[5], f16), pack2(o[6], o[7], f16));
+          } else {
+            part[(int64_t)(8 * c + 2 * i) * R] = make_float4(o[0], o[1], o[2], o[3]);
+            part[(int64_t)(8 * c + 2 * i + 1) * R] = make_float4(o[4], o[5], o[6], o[7]);
           }
         }
       }
       if (whole) {
-        if (ok && a.lse) a.lse[tok * a.Hq + hq] = lse2 * (1.f / kLog2e);
+        rows_out();
+        if (ok && a.lse) a.lse[lse_at] = lse2 * (1.f / kLog2e);
       } else {
-        if (r < rows) ws.lse[slot * R + r] = lse2;
+        ws.lse[slot * R + r] = lse2;
+        // the CTA that finishes its part of the unit last joins the parts, in their order
+        const int c0 = share_owner(W, C, cur.u0), c1 = share_owner(W, C, ue - 1);
         __threadfence();
-      }
-      tc::fence_before_sync();
-    }
-
-    if (!(x == cur.u0 && xe == ue)) {
-      // the CTA that finishes its part of the unit last joins the parts, in their order
-      const int c0 = share_owner(W, C, cur.u0), c1 = share_owner(W, C, ue - 1);
-      __syncthreads();
-      if (tid == 0) {
-        __threadfence();
-        sh.last = atomicInc(reinterpret_cast<unsigned*>(&ws.count[c0]), (unsigned)(c1 - c0)) == (unsigned)(c1 - c0);
-        __threadfence();
-      }
-      __syncthreads();
-      if (sh.last) {
-        auto slot_of = [&](int p) { return p == c0 ? 2 * p + 1 : 2 * p; };
-        constexpr int Q4 = D / 4;
-        for (int i = tid; i < rows * Q4; i += NTH) {
-          const int r = i / Q4, k = i % Q4;
+        tc::bar_sync(1 + wg, 128);
+        if ((r & 127) == 0) {
+          __threadfence();
+          sh.last[wg] = atomicInc(reinterpret_cast<unsigned*>(&ws.count[2 * c0 + wg]), (unsigned)(c1 - c0)) == (unsigned)(c1 - c0);
+          __threadfence();
+        }
+        tc::bar_sync(1 + wg, 128);
+        if (sh.last[wg]) {
+          auto slot_of = [&](int p) { return p == c0 ? 2 * p + 1 : 2 * p; };
           float m = -INFINITY, L = 0.f;
           for (int p = c0; p <= c1; ++p) m = fmaxf(m, __ldcg(&ws.lse[slot_of(p) * R + r]));
           const float mu = m == -INFINITY ? 0.f : m;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int p = c0; p <= c1; ++p) {
-            const float w = ex2(__ldcg(&ws.lse[slot_of(p) * R + r]) - mu);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(ws.o + ((int64_t)slot_of(p) * R + r) * D) + k);
-            L += w;
-            o.x = fmaf(v.x, w, o.x);
-            o.y = fmaf(v.y, w, o.y);
-            o.z = fmaf(v.z, w, o.z);
-            o.w = fmaf(v.w, w, o.w);
-          }
-          const float inv = L > 0.f ? 1.f / L : 0.f;
-          const int row = cur.rg * R + r;
-          const int64_t tok = (int64_t)cur.s.q0 + row / G;
-          const int hq = cur.h * G + row % G;
-          if (tok >= 0 && tok < a.total_q) {
-            const int64_t at = (tok * a.Hq + hq) * D + 4 * k;
-            if (g.dtype == TQ_F16) {
-              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-                  make_uint2(pack_half(o.x * inv, o.y * inv), pack_half(o.z * inv, o.w * inv));
-            } else {
-              const __nv_bfloat162 b0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), b1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-                  make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+          for (int p = c0; p <= c1; ++p) L += ex2(__ldcg(&ws.lse[slot_of(p) * R + r]) - mu);
+          const float iL = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll 1
+          for (int c = 0; c < D / 8; ++c) {
+            float4 o0 = make_float4(0.f, 0.f, 0.f, 0.f), o1 = o0;
+            for (int p = c0; p <= c1; ++p) {
+              const float w = ex2(__ldcg(&ws.lse[slot_of(p) * R + r]) - mu) * iL;
+              const float4* src = reinterpret_cast<const float4*>(ws.o + (int64_t)slot_of(p) * R * D) + r;
+              const float4 u0 = __ldcg(src + (int64_t)(2 * c) * R), u1 = __ldcg(src + (int64_t)(2 * c + 1) * R);
+              o0.x = fmaf(u0.x, w, o0.x);
+              o0.y = fmaf(u0.y, w, o0.y);
+              o0.z = fmaf(u0.z, w, o0.z);
+              o0.w = fmaf(u0.w, w, o0.w);
+              o1.x = fmaf(u1.x, w, o1.x);
+              o1.y = fmaf(u1.y, w, o1.y);
+              o1.z = fmaf(u1.z, w, o1.z);
+              o1.w = fmaf(u1.w, w, o1.w);
             }
-            if (a.lse && k == 0) a.lse[tok * a.Hq + hq] = L > 0.f ? (m + log2f(L)) * (1.f / kLog2e) : -INFINITY;
+            *reinterpret_cast<uint4*>(Q + sw_off<128>(r & 127, c)) =
+                make_uint4(pack2(o0.x, o0.y, f16), pack2(o0.z, o0.w, f16), pack2(o1.x, o1.y, f16), pack2(o1.z, o1.w, f16));
           }
+          rows_out();
+          if (ok && a.lse)
+            a.lse[lse_at] =
+                L > 0.f ? (m + log2f(L)) * (1.f / kLog2e) : -INFINITY;
         }
       }
-    }
-    n0 += nt;
-    x = xe;
-    if (x < x1) next_unit<R, T>(g, a, G, cur);
+      tc::fence_before_sync();
+    });
   }
   __syncthreads();
   if (is_mma) {
@@ -586,7 +673,7 @@ cudaError_t chunk_t(const PGeom& g, const PagedAttn& a, cudaStream_t s) {
   constexpr size_t smem = chunk_smem<D, MT>();
   cudaError_t e = cudaFuncSetAttribute(k_paged_chunk<D, CODE, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_paged_chunk<D, CODE, MT>, dim3(kChunkCtas), dim3(128 * MT + 128), smem, s, g, a);
+  return launch_pdl(k_paged_chunk<D, CODE, MT>, dim3(kChunkCtas), dim3(128 * MT + 256), smem, s, g, a);
 }
 
 template <int D>
