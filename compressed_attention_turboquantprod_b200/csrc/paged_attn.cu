@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
   constexpr float kUp = 32768.f;           // p is held times 2^15: its halves reach 2^-40
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) uint64_t s_full[kDecWarps][NST];
-  __shared__ int64_t s_sum[kDecWarps];
+  __shared__ SplitPlan s_plan;
   __shared__ Cursor s_cur;
   __shared__ float s_fr[kDecRows];
   __shared__ int s_vis[kDecRows];
@@ -102,14 +102,14 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
     return;
   }
   if (cta_first_checks(g, a)) atomicOr(&g.state->status, kPagedBadOffsets);
-  const int64_t W = count_tiles<kDecRows, kTile, kDecThreads>(g, a, G, s_sum);
+  const int64_t W = count_places<kDecRows, kTile, 0, kDecThreads>(g, a, G, s_plan);
   if (W == 0) return;
   const int64_t C = share_ctas(W, gridDim.x, kDecWarps);
   const int cta = blockIdx.x;
   if (cta >= C) return;
   const int64_t x0 = share_begin(W, C, cta), x1 = share_begin(W, C, cta + 1);
   if (warp == 0) {
-    const Cursor f = find_unit<kDecRows, kTile>(g, a, G, x0);
+    const Cursor f = find_unit<kDecRows, kTile, 0>(g, a, G, x0, s_plan);
     if (lane == 0) s_cur = f;
   }
   __syncthreads();
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
   auto look = [&]() {                       // the tile at xi: its unit, and this lane's sub-block
     nvis = 0;
     if (xi >= x1) return;
-    while (xi >= nxt.u0 + nxt.nt) next_unit<kDecRows, kTile>(g, a, G, nxt);
+    while (xi >= nxt.u0 + nxt.nt) next_unit<kDecRows, kTile, 0>(g, a, G, nxt);
     nvis = group_visible<kDecRows>(nxt.s, G, nxt.rg, a.causal);
     if (nvis > 0 && lane < NSUB) {
       // sub-blocks past the end repeat the last one: masked, but finite
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
       }
     }
     x = xe;
-    if (x < x1) next_unit<kDecRows, kTile>(g, a, G, cur);
+    if (x < x1) next_unit<kDecRows, kTile, 0>(g, a, G, cur);
   }
   if (s_abort) {
     // a wait gave up: let the copies in flight land before the shared memory is given back

@@ -33,13 +33,13 @@ constexpr float kNone = -1e30f;            // reference of a row that has seen n
 constexpr float kBias = 11.f;              // p is held times 2^11
 constexpr float kSlack = 4.f;
 
-template <int D>
-__host__ __device__ constexpr int chunk_tokens() { return D == 256 ? 64 : 128; }
+constexpr int kTokens = 64;                // tokens of a tile
+constexpr int kUnitCost = 4;               // places of a unit besides its tiles
 template <int D>
 __host__ __device__ constexpr int chunk_max_mt() { return D == 256 ? 1 : 2; }
 template <int D, int MT>
 __host__ __device__ constexpr size_t chunk_smem() {
-  return 1024 + (size_t)MT * 128 * D * 2 + 4 * (size_t)chunk_tokens<D>() * D * 2;
+  return 1024 + (size_t)MT * 128 * D * 2 + 4 * (size_t)kTokens * D * 2;
 }
 
 // Operands lie in shared memory K-major in the 128-byte swizzle: slabs of 64 f16 along K, a row
@@ -111,10 +111,10 @@ __device__ __forceinline__ ChunkWs chunk_ws(void* ws) {
 
 template <int MT>
 struct ChunkShared {
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_ready[2], pv_done[2], q_full[2];
-  uint64_t scales[4];
-  int64_t sum[4 * MT + 8];
-  float sk[4][8], lv[4][8];                // a tile's scales per 16 tokens: of the keys, log2 of the values'
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], scales[4];
+  uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];      // [row block][tile mod 2]
+  SplitPlan plan;
+  float sk[4][4], lv[4][4];                // a tile's scales per 16 tokens: of the keys, log2 of the values'
   float fr[128 * MT];                      // a row's factor on S
   Cursor cur;
   uint32_t tmem;
@@ -126,6 +126,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// 16 columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
       : "memory");
 }
 
@@ -155,7 +166,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, bool f16) {
 
 template <int D, int CODE, int MT>
 __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, PagedAttn a) {
-  constexpr int T = chunk_tokens<D>(), R = 128 * MT, NTH = R + 256;
+  constexpr int T = kTokens, R = 128 * MT, NTH = R + 256;
   constexpr int TW = T / kConv;                       // tokens of a tile a converter warp expands
   constexpr int NK = T * D / 16 / 128;                // 16-byte pieces of a tile's keys (values) per converter lane
   constexpr uint32_t kTb = T * D * 2;                 // bytes of an f16 operand tile
@@ -175,10 +186,12 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       mbar_init(&sh.k_free[i], 1);
       mbar_init(&sh.v_full[i], kConv);
       mbar_init(&sh.v_free[i], 1);
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_ready[i], 4);
-      mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.q_full[i], 4);
+      for (int w = 0; w < 2; ++w) {
+        mbar_init(&sh.s_full[w][i], 1);
+        mbar_init(&sh.p_ready[w][i], 4);
+        mbar_init(&sh.pv_done[w][i], 1);
+      }
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sh.abort = 0;
@@ -191,14 +204,14 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
     return;
   }
   if (cta_first_checks(g, a)) atomicOr(&g.state->status, kPagedBadOffsets);
-  const int64_t W = count_tiles<R, T, NTH>(g, a, G, sh.sum);
+  const int64_t W = count_places<R, T, kUnitCost, NTH>(g, a, G, sh.plan);
   if (W == 0) return;
-  const int64_t C = share_ctas(W, gridDim.x, 2);
+  const int64_t C = share_ctas(W, gridDim.x, kUnitCost + 2);
   const int cta = blockIdx.x;
   if (cta >= C) return;
   const int64_t x0 = share_begin(W, C, cta), x1 = share_begin(W, C, cta + 1);
   if (warp == 0) {
-    const Cursor f = find_unit<R, T>(g, a, G, x0);
+    const Cursor f = find_unit<R, T, kUnitCost>(g, a, G, x0, sh.plan);
     if (lane == 0) sh.cur = f;
   }
   if (is_mma) {
@@ -217,19 +230,21 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       atomicOr(&g.state->status, kPagedWait);
     }
   };
-  // Each role walks the CTA's units by itself: f(first tile of the segment in its unit, tiles of the
-  // segment (0 for a unit that sees nothing), tiles of the CTA before it, segments with tiles before it).
+  // Each role walks the CTA's units by itself: f(tiles of the unit in this CTA's share, how many of
+  // them are to be worked on (none in a unit that sees nothing), such tiles before, segments with such tiles before).
   auto walk = [&](auto f) {
     int64_t x = x0;
     int n0 = 0, seg = 0;
     while (x < x1) {
-      const int64_t xe = min(x1, cur.u0 + cur.nt);
-      const int nt = group_visible<R>(cur.s, G, cur.rg, a.causal) > 0 ? (int)(xe - x) : 0;
-      f(x, xe, nt, n0, seg);
-      n0 += nt;
-      seg += nt > 0;
-      x = xe;
-      if (x < x1) next_unit<R, T>(g, a, G, cur);
+      const Segment<kUnitCost> sg(cur, x, x1);
+      if (!sg.empty()) {
+        const int nt = group_visible<R>(cur.s, G, cur.rg, a.causal) > 0 ? sg.last - sg.first : 0;
+        f(sg, nt, n0, seg);
+        n0 += nt;
+        seg += nt > 0;
+      }
+      x = min(x1, cur.u0 + kUnitCost + cur.nt);
+      if (x < x1) next_unit<R, T, kUnitCost>(g, a, G, cur);
     }
   };
 
@@ -259,9 +274,9 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
       *reinterpret_cast<uint4*>(to2) = make_uint4(o[4], o[5], o[6], o[7]);
     };
-    walk([&](int64_t x, int64_t, int nt, int n0, int) {
+    walk([&](const auto& sg, int nt, int n0, int) {
       if (nt == 0) return;
-      const int tok0 = (int)(x - cur.u0) * T + cw * TW, last = cur.s.len - 1;
+      const int tok0 = sg.first * T + cw * TW, last = cur.s.len - 1;
       const int* table = g.table + (int64_t)cur.s.slot * g.max_pages;
       uint4 kr[NK], vr[NK];
       int pid[NH], off[NH];                           // page and token offset in it of each half, a tile ahead
@@ -346,73 +361,48 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dQ = sw_desc(__shfl_sync(0xffffffffu, sQ, 0)), dK = sw_desc(__shfl_sync(0xffffffffu, sK, 0)),
                    dV = sw_desc(__shfl_sync(0xffffffffu, sV, 0));
-    auto qk = [&](int w, int sb, int b2) {
+    auto qk = [&](int w, int b2) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
-        mma_ss(tm + cS + sb * T, dQ + (uint64_t)(w * (128 * D * 2 / 16) + sw_step<128>(k)),
+        mma_ss(tm + cS + (2 * w + b2) * T, dQ + (uint64_t)(w * (128 * D * 2 / 16) + sw_step<128>(k)),
                dK + (uint64_t)(b2 * (kTb / 16) + sw_step<T>(k)), iS, k > 0);
     };
-    auto pv = [&](int w, int sb, int b2, bool first) {
+    auto pv = [&](int w, int b2, bool first) {
 #pragma unroll
       for (int k = 0; k < T / 16; ++k)
-        mma_ts(tm + cO + w * D, tm + cS + sb * T + 8 * k, dV + (uint64_t)(b2 * (kTb / 16) + sw_step<D>(k)), iO,
+        mma_ts(tm + cO + w * D, tm + cS + (2 * w + b2) * T + 8 * k, dV + (uint64_t)(b2 * (kTb / 16) + sw_step<D>(k)), iO,
                !(first && k == 0));
     };
-    walk([&](int64_t, int64_t, int nt_, int n0_, int seg_) {
+    walk([&](const auto&, int nt_, int n0_, int seg_) {
       const int nt = __shfl_sync(0xffffffffu, nt_, 0), n0 = __shfl_sync(0xffffffffu, n0_, 0),
                 seg = __shfl_sync(0xffffffffu, seg_, 0);
-      if (nt == 0) return;
-      // q_full: the row block's queries are in place, and its last unit's O has been read
-      if constexpr (MT == 2) {
-        wait(&sh.k_full[n0 & 1], n0 >> 1);
+      // Q K^T of tile n + 1, then P V of tile n: the tensor cores have work while the softmax of n runs
+      for (int t = -1; t < nt; ++t) {
+        const int n = n0 + t, m = n + 1;
+        if (t + 1 < nt) {
+          wait(&sh.k_full[m & 1], m >> 1);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          wait(&sh.q_full[w], seg);
-          tc::fence_after_sync();
-          qk(w, w, n0 & 1);
-          mma_commit_elected(&sh.s_full[w]);
+          for (int w = 0; w < MT; ++w) {
+            // the row block's queries are in place and its last unit's O has been read; or P of tile
+            // n - 1, over this S buffer, has been used
+            if (t < 0) wait(&sh.q_full[w], seg);
+            if (t >= 1) wait(&sh.pv_done[w][m & 1], (n - 1) >> 1);
+            tc::fence_after_sync();
+            qk(w, m & 1);
+            mma_commit_elected(&sh.s_full[w][m & 1]);
+          }
+          mma_commit_elected(&sh.k_free[m & 1]);
         }
-        mma_commit_elected(&sh.k_free[n0 & 1]);
-        for (int t = 0; t < nt; ++t) {
-          const int n = n0 + t, b2 = n & 1, m = n + 1;
-          wait(&sh.v_full[b2], n >> 1);
+        if (t >= 0) {
+          wait(&sh.v_full[n & 1], n >> 1);
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            wait(&sh.p_ready[w], n);
+          for (int w = 0; w < MT; ++w) {
+            wait(&sh.p_ready[w][n & 1], n >> 1);
             tc::fence_after_sync();
-            pv(w, w, b2, t == 0);
-            mma_commit_elected(&sh.pv_done[w]);
-            if (w == 1) mma_commit_elected(&sh.v_free[b2]);
-            if (t + 1 < nt) {
-              if (w == 0) wait(&sh.k_full[m & 1], m >> 1);
-              wait(&sh.pv_done[w], n);              // P_w lies over S_w
-              tc::fence_after_sync();
-              qk(w, w, m & 1);
-              mma_commit_elected(&sh.s_full[w]);
-              if (w == 1) mma_commit_elected(&sh.k_free[m & 1]);
-            }
+            pv(w, n & 1, t == 0);
+            mma_commit_elected(&sh.pv_done[w][n & 1]);
           }
-        }
-      } else {
-        wait(&sh.q_full[0], seg);
-        for (int t = -1; t < nt; ++t) {
-          const int n = n0 + t, m = n + 1;
-          if (t + 1 < nt) {
-            wait(&sh.k_full[m & 1], m >> 1);
-            if (t >= 1) wait(&sh.pv_done[m & 1], (n - 1) >> 1);      // its P lies over this S buffer
-            tc::fence_after_sync();
-            qk(0, m & 1, m & 1);
-            mma_commit_elected(&sh.s_full[m & 1]);
-            mma_commit_elected(&sh.k_free[m & 1]);
-          }
-          if (t >= 0) {
-            wait(&sh.v_full[n & 1], n >> 1);
-            wait(&sh.p_ready[n & 1], n >> 1);
-            tc::fence_after_sync();
-            pv(0, n & 1, n & 1, t == 0);
-            mma_commit_elected(&sh.pv_done[n & 1]);
-            mma_commit_elected(&sh.v_free[n & 1]);
-          }
+          mma_commit_elected(&sh.v_free[n & 1]);
         }
       }
     });
@@ -429,9 +419,8 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
     auto by_g = [&](int row) { return G == 1 ? row : (int)__umulhi((uint32_t)row, gm); };
     // rows of D / 8 16-byte pieces: RL lanes a row, RI rows an instruction
     constexpr int RL = D / 8, RI = 32 / RL;
-    walk([&](int64_t x, int64_t xe, int nt, int n0, int) {
-      const int64_t ue = cur.u0 + cur.nt;
-      const int tok0 = (int)(x - cur.u0) * T;          // the segment's first token
+    walk([&](const auto& sg, int nt, int n0, int) {
+      const int tok0 = sg.first * T;                   // the segment's first token
       const int rows = (int)min((int64_t)R, (int64_t)cur.s.nq * G - (int64_t)cur.rg * R);
       const int row0 = cur.rg * R;                     // the CTA's first row of the sequence (below 2^27)
       // place of CTA row i's D entries in Q and out (heads of a token lie side by side); -1: none
@@ -478,101 +467,93 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         if (lane == 0) mbar_arrive(&sh.q_full[wg]);
         fr = ok ? sh.fr[r] : 0.f;
       }
-      // A parity tells a completion only from its neighbours, so every waiter has to be within one
-      // of it.  MT = 2: S_w of tile n came after the products P V of n - 1.  MT = 1: after those of
-      // n - 2 only, hence a barrier per buffer.
-      auto pv_wait = [&](int n) {
-        if (MT == 2) wait(&sh.pv_done[wg], n); else wait(&sh.pv_done[n & 1], n >> 1);
-      };
+      // A parity tells a completion only from its neighbours, so every waiter has to be within one of
+      // it: S of tile n came after P V of n - 2 only, hence a barrier per buffer.
+      auto pv_wait = [&](int n) { wait(&sh.pv_done[wg][n & 1], n >> 1); };
       // the rows of the warp see at least wmin tokens
       const int wmin = __reduce_min_sync(0xffffffffu, vis);
       for (int t = 0; t < nt; ++t) {
         const int n = n0 + t, sc = n & 3;
-        const uint32_t tS = tmem + lrow + cS + (MT == 2 ? wg : n & 1) * T;
+        const uint32_t tS = tmem + lrow + cS + (2 * wg + (n & 1)) * T;
         const int base = tok0 + t * T;                 // the tile's first token
         wait(&sh.scales[sc], n >> 2);
-        if (MT == 2) wait(&sh.s_full[wg], n); else wait(&sh.s_full[n & 1], n >> 1);
+        wait(&sh.s_full[wg][n & 1], n >> 1);
         tc::fence_after_sync();
         if (t == 0) lvr = sh.lv[sc][0];
-        // S in pieces of 32 columns, the next requested while one is worked on
-        auto columns = [&](auto f) {
-          uint32_t v[2][32];
-          tc::tmem_ld32(tS, v[0]);
-          tmem_wait_ld(v[0]);
+        uint32_t v[2][32];                             // the row of S
+        tc::tmem_ld32(tS, v[0]);
+        tc::tmem_ld32(tS + 32, v[1]);
+        tmem_wait_ld(v[0]);
+        tmem_wait_ld(v[1]);
+        if (base + T > wmin) {                         // a tile that not every row of the warp sees in full
 #pragma unroll
-          for (int c = 0; c < T / 32; ++c) {
-            if (c + 1 < T / 32) tc::tmem_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
-            f(c, v[c & 1]);
-            if (c + 1 < T / 32) tmem_wait_ld(v[(c + 1) & 1]);
-          }
-        };
-        auto both_passes = [&](auto MASK) {
-          auto hide = [&](int col, float z) { return !decltype(MASK)::value || base + col < vis ? z : -INFINITY; };
-          // the largest exponent f S + log2 s_v
-          float zmax = -INFINITY;
-          columns([&](int c, const uint32_t (&v)[32]) {
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float m = -INFINITY;
+            for (int i = 0; i < 32; ++i)
+              if (base + 32 * c + i >= vis) v[c][i] = 0xff800000u;
+        }
+        float f[T / 16], lv[T / 16], zmax = -INFINITY;  // the largest exponent f S + log2 s_v
 #pragma unroll
-              for (int i = 0; i < 16; ++i) m = fmaxf(m, hide(32 * c + 16 * h + i, __uint_as_float(v[16 * h + i])));
-              const float z = fmaf(m, fr * sh.sk[sc][2 * c + h], sh.lv[sc][2 * c + h]);
-              zmax = fmaxf(zmax, m == -INFINITY ? m : z);
-            }
-          });
-          if (__any_sync(0xffffffffu, M == kNone ? zmax > -INFINITY : zmax > M + kSlack)) {
-            const float Mn = M == kNone ? (zmax == -INFINITY ? kNone : zmax) : fmaxf(M, zmax);
-            const float alpha = M == kNone ? 0.f : ex2(M - Mn);
-            M = Mn;
-            l *= alpha;
-            if (t > 0) {
-              pv_wait(n - 1);
-              tc::fence_after_sync();
+        for (int h = 0; h < T / 16; ++h) {
+          f[h] = fr * sh.sk[sc][h];
+          lv[h] = sh.lv[sc][h];
+          float m = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) m = fmaxf(m, __uint_as_float(v[h >> 1][16 * (h & 1) + i]));
+          zmax = fmaxf(zmax, m == -INFINITY ? m : fmaf(m, f[h], lv[h]));
+        }
+        if (__any_sync(0xffffffffu, M == kNone ? zmax > -INFINITY : zmax > M + kSlack)) {
+          const float Mn = M == kNone ? (zmax == -INFINITY ? kNone : zmax) : fmaxf(M, zmax);
+          const float alpha = M == kNone ? 0.f : ex2(M - Mn);
+          M = Mn;
+          l *= alpha;
+          if (t > 0) {
+            pv_wait(n - 1);
+            tc::fence_after_sync();
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t v[32];
-                tc::tmem_ld32(tO + 32 * c, v);
-                tmem_wait_ld(v);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16 * c, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-                tc::tmem_st32(tO + 32 * c, v);
-              }
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st16(tO + 16 * c, o);
             }
           }
-          // p and its sum; 32 columns of S give 16 of P, which lie over columns already read
-          columns([&](int c, const uint32_t (&v)[32]) {
-            uint32_t pk[16];
+        }
+        // p and its sum.  A masked S is -inf: its product with f = 0 (an unused row, a block of
+        // zeros) would be NaN, so such a row's f counts as the smallest factor instead
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float f = fr * sh.sk[sc][2 * c + h], lv = sh.lv[sc][2 * c + h], cst = lv - M + kBias;
-              const float2 f2 = make_float2(f, f), c2 = make_float2(cst, cst);
-              float2 ls = make_float2(0.f, 0.f);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int col = 32 * c + 16 * h + 2 * i;
-                float2 z = fma2(make_float2(__uint_as_float(v[16 * h + 2 * i]), __uint_as_float(v[16 * h + 2 * i + 1])), f2, c2);
-                const float2 p = make_float2(ex2(hide(col, z.x)), ex2(hide(col + 1, z.y)));
-                ls = add2(ls, p);
-                pk[8 * h + i] = pack_half(p.x, p.y);
-              }
-              l = fmaf(ls.x + ls.y, ex2(lvr - lv), l);
+          for (int e = 0; e < 2; ++e) {
+            const int h = 2 * c + e;
+            const float ff = fmaxf(f[h], 1.1754944e-38f), cst = lv[h] - M + kBias;
+            const float2 f2 = make_float2(ff, ff), c2 = make_float2(cst, cst);
+            float2 ls = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 z = fma2(make_float2(__uint_as_float(v[c][16 * e + 2 * i]), __uint_as_float(v[c][16 * e + 2 * i + 1])), f2, c2);
+              const float2 p = make_float2(ex2(z.x), ex2(z.y));
+              ls = add2(ls, p);
+              pk[8 * e + i] = pack_half(p.x, p.y);
             }
-            tmem_st16(tS + 16 * c, pk);
-          });
-        };
-        if (base + T > wmin) both_passes(std::true_type()); else both_passes(std::false_type());
+            l = fmaf(ls.x + ls.y, ex2(lvr - lv[h]), l);
+          }
+          tmem_st16(tS + 16 * c, pk);
+        }
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
         // (a warp may finish tile n + 1 before another has finished n, but not n + 2)
-        if (lane == 0) mbar_arrive(&sh.p_ready[MT == 2 ? wg : n & 1]);
+        if (lane == 0) mbar_arrive(&sh.p_ready[wg][n & 1]);
       }
       // ---- the row's output, or its part
-      const bool whole = x == cur.u0 && xe == ue;
+      const bool whole = sg.whole(cur);
       const float inv = l > 0.f ? ex2(lvr) / l : 0.f;
       const float lse2 = l > 0.f ? log2f(l) + (M - lvr - kBias) : -INFINITY;
       const int64_t lse_at = ((int64_t)cur.s.q0 + by_g(row0 + r)) * a.Hq + cur.h * G + row0 + r - by_g(row0 + r) * G;
-      const int slot = 2 * cta + (x == cur.u0 ? 1 : 0);
+      const int slot = 2 * cta + (sg.first == 0 ? 1 : 0);
       if (nt > 0) {
         pv_wait(n0 + nt - 1);                          // (and so the row block's products with Q are done)
         tc::fence_after_sync();
@@ -617,7 +598,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       } else {
         ws.lse[slot * R + r] = lse2;
         // the CTA that finishes its part of the unit last joins the parts, in their order
-        const int c0 = share_owner(W, C, cur.u0), c1 = share_owner(W, C, ue - 1);
+        const int c0 = share_owner(W, C, cur.u0 + kUnitCost), c1 = share_owner(W, C, cur.u0 + kUnitCost + cur.nt - 1);
         __threadfence();
         tc::bar_sync(1 + wg, 128);
         if ((r & 127) == 0) {
@@ -633,24 +614,32 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
           const float mu = m == -INFINITY ? 0.f : m;
           for (int p = c0; p <= c1; ++p) L += ex2(__ldcg(&ws.lse[slot_of(p) * R + r]) - mu);
           const float iL = L > 0.f ? 1.f / L : 0.f;
+          // 32 channels at a time: eight reads in flight per part
 #pragma unroll 1
-          for (int c = 0; c < D / 8; ++c) {
-            float4 o0 = make_float4(0.f, 0.f, 0.f, 0.f), o1 = o0;
+          for (int c = 0; c < D / 32; ++c) {
+            float4 o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
             for (int p = c0; p <= c1; ++p) {
+              const float4* src = reinterpret_cast<const float4*>(ws.o + (int64_t)slot_of(p) * R * D) + (int64_t)(8 * c) * R + r;
+              float4 u[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) u[k] = __ldcg(src + (int64_t)k * R);
               const float w = ex2(__ldcg(&ws.lse[slot_of(p) * R + r]) - mu) * iL;
-              const float4* src = reinterpret_cast<const float4*>(ws.o + (int64_t)slot_of(p) * R * D) + r;
-              const float4 u0 = __ldcg(src + (int64_t)(2 * c) * R), u1 = __ldcg(src + (int64_t)(2 * c + 1) * R);
-              o0.x = fmaf(u0.x, w, o0.x);
-              o0.y = fmaf(u0.y, w, o0.y);
-              o0.z = fmaf(u0.z, w, o0.z);
-              o0.w = fmaf(u0.w, w, o0.w);
-              o1.x = fmaf(u1.x, w, o1.x);
-              o1.y = fmaf(u1.y, w, o1.y);
-              o1.z = fmaf(u1.z, w, o1.z);
-              o1.w = fmaf(u1.w, w, o1.w);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                o[k].x = fmaf(u[k].x, w, o[k].x);
+                o[k].y = fmaf(u[k].y, w, o[k].y);
+                o[k].z = fmaf(u[k].z, w, o[k].z);
+                o[k].w = fmaf(u[k].w, w, o[k].w);
+              }
             }
-            *reinterpret_cast<uint4*>(Q + sw_off<128>(r & 127, c)) =
-                make_uint4(pack2(o0.x, o0.y, f16), pack2(o0.z, o0.w, f16), pack2(o1.x, o1.y, f16), pack2(o1.z, o1.w, f16));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(Q + sw_off<128>(r & 127, 4 * c + k)) =
+                  make_uint4(pack2(o[2 * k].x, o[2 * k].y, f16), pack2(o[2 * k].z, o[2 * k].w, f16),
+                             pack2(o[2 * k + 1].x, o[2 * k + 1].y, f16), pack2(o[2 * k + 1].z, o[2 * k + 1].w, f16));
           }
           rows_out();
           if (ok && a.lse)

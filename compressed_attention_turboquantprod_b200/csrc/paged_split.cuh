@@ -14,12 +14,13 @@ constexpr uint32_t kWsMagic = 0x70384b56u;
 constexpr size_t kWsHeader = 4096;
 
 // ---------------------------------------------------------------- the split over CTAs
-// The work of a call is a list of tiles of T tokens, in the order (sequence, group of query
-// rows, head, tile); a unit is one (sequence, group, head), at least one tile long so that a
-// unit that sees nothing is also written.  Every CTA takes an equal, contiguous share of the
-// list, whatever the lengths: a CTA's share may begin and end inside a unit, and then leaves a
-// partial (m, l, o) for the CTA that finishes that unit last.  Lengths are read on the device,
-// so a captured call follows them.
+// The work of a call is a list of places, in the order (sequence, group of query rows, head); a
+// unit is one (sequence, group, head) and has KO + nt places, nt its tiles of T tokens (at least one, so
+// that a unit that sees nothing is also written).  The KO places before a unit's tiles stand for
+// what a unit costs besides them (queries in, output out), in tiles.  Every CTA takes an equal, contiguous
+// share of the list, whatever the lengths: a share may begin and end inside a unit, and then leaves
+// a partial output for the CTA that finishes that unit last.  Lengths are read on the device, so a
+// captured call follows them.
 struct Seq {
   int slot, len, nq, q0;
 };
@@ -63,93 +64,125 @@ __device__ __forceinline__ bool cta_first_checks(const PGeom& g, const PagedAttn
   return bad;
 }
 
-struct Cursor {      // a unit: its place in the list, and what it is
+struct Cursor {      // a unit: its first place in the list, its tiles, and what it is
   int64_t u0;
   int nt, i, rg, h;
   Seq s;
 };
 
-// Tiles of sequence i, by one thread: a causal sequence's groups see one run of lengths.
-template <int R, int T>
-__device__ int64_t seq_tiles(const PGeom& g, const PagedAttn& a, int i, int G) {
+// Places of one head of sequence i: by one thread, or by a whole warp (every lane gets the sum).
+template <int R, int T, int KO>
+__device__ __forceinline__ int64_t head_places(const PGeom& g, const PagedAttn& a, int i, int G) {
   const Seq s = load_seq(g, a, i);
   const int ng = seq_groups<R>(s, G);
   if (ng == 0) return 0;
-  if (!a.causal || s.nq == 1) return (int64_t)g.Hkv * ng * group_tiles<R, T>(s, G, 0, a.causal);
+  if (ng == 1 || !a.causal) return (int64_t)ng * (KO + group_tiles<R, T>(s, G, 0, a.causal));
   int64_t t = 0;
-  for (int rg = 0; rg < ng; ++rg) t += group_tiles<R, T>(s, G, rg, a.causal);
-  return g.Hkv * t;
+  for (int rg = 0; rg < ng; ++rg) t += KO + group_tiles<R, T>(s, G, rg, a.causal);
+  return t;
 }
-
-// All threads of the CTA (NT): the number of tiles of the call.
-template <int R, int T, int NT>
-__device__ int64_t count_tiles(const PGeom& g, const PagedAttn& a, int G, int64_t* s_sum) {
+template <int R, int T, int KO>
+__device__ __forceinline__ int64_t head_places_warp(const PGeom& g, const PagedAttn& a, int i, int G) {
+  const Seq s = load_seq(g, a, i);
+  const int ng = seq_groups<R>(s, G);
+  if (ng == 0) return 0;
+  if (!a.causal) return (int64_t)ng * (KO + group_tiles<R, T>(s, G, 0, a.causal));
   int64_t t = 0;
-  for (int i = threadIdx.x; i < a.n; i += NT) t += seq_tiles<R, T>(g, a, i, G);
+  for (int rg = threadIdx.x & 31; rg < ng; rg += 32) t += KO + group_tiles<R, T>(s, G, rg, a.causal);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = t;
-  __syncthreads();
-  t = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) t += s_sum[w];
   return t;
 }
 
-// One warp: the unit that holds tile x of the list.
-template <int R, int T>
-__device__ Cursor find_unit(const PGeom& g, const PagedAttn& a, int G, int64_t x) {
+// Shared memory of the plan: the sequences' places, when there are at most kPlanSeqs of them.
+constexpr int kPlanSeqs = 128;
+struct SplitPlan {
+  int64_t sum[16];
+  int64_t places[kPlanSeqs];
+};
+
+// All threads of the CTA (NT): the places of the call.
+template <int R, int T, int KO, int NT>
+__device__ int64_t count_places(const PGeom& g, const PagedAttn& a, int G, SplitPlan& sp) {
+  int64_t t = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((int64_t)a.max_q * G > R) {               // several groups: a warp per sequence
+    for (int i = warp; i < a.n; i += NT / 32) {
+      const int64_t v = g.Hkv * head_places_warp<R, T, KO>(g, a, i, G);
+      if (lane == 0) {
+        t += v;
+        if (i < kPlanSeqs) sp.places[i] = v;
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < a.n; i += NT) {
+      const int64_t v = g.Hkv * head_places<R, T, KO>(g, a, i, G);
+      t += v;
+      if (i < kPlanSeqs) sp.places[i] = v;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if (lane == 0) sp.sum[warp] = t;
+  __syncthreads();
+  t = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) t += sp.sum[w];
+  return t;
+}
+
+// Over 32 values, one per lane: the lane whose running sum (from `base`) first passes x, and the
+// sum before it in `base`; -1: none, all of them are in `base`.
+__device__ __forceinline__ int find_lane(int64_t t, int64_t& base, int64_t x) {
+  const int lane = threadIdx.x & 31;
+  int64_t v = t;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  const unsigned hit = __ballot_sync(0xffffffffu, base + v > x);
+  const int l = hit ? __ffs(hit) - 1 : 31;
+  base += __shfl_sync(0xffffffffu, hit ? v - t : v, l);
+  return hit ? l : -1;
+}
+
+// One warp, after count_places: the unit that holds place x of the list.
+template <int R, int T, int KO>
+__device__ Cursor find_unit(const PGeom& g, const PagedAttn& a, int G, int64_t x, const SplitPlan& sp) {
   const int lane = threadIdx.x & 31;
   int64_t base = 0;
   Cursor c{};
-  int i = 0;
   for (int i0 = 0; i0 < a.n; i0 += 32) {
-    const int64_t t = i0 + lane < a.n ? seq_tiles<R, T>(g, a, i0 + lane, G) : 0;
-    int64_t v = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, base + v > x);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      base += __shfl_sync(0xffffffffu, v - t, l);
-      i = i0 + l;
+    const int i = i0 + lane;
+    const int64_t t = i >= a.n ? 0 : i < kPlanSeqs ? sp.places[i] : g.Hkv * head_places<R, T, KO>(g, a, i, G);
+    const int l = find_lane(t, base, x);
+    if (l >= 0) {
+      c.i = i0 + l;
       break;
     }
-    base += __shfl_sync(0xffffffffu, v, 31);
   }
-  c.i = i;
-  c.s = load_seq(g, a, i);
+  c.s = load_seq(g, a, c.i);
   const int ng = seq_groups<R>(c.s, G);
   for (int r0 = 0; r0 < ng; r0 += 32) {
-    const int64_t t = r0 + lane < ng ? (int64_t)g.Hkv * group_tiles<R, T>(c.s, G, r0 + lane, a.causal) : 0;
-    int64_t v = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, base + v > x);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      base += __shfl_sync(0xffffffffu, v - t, l);
+    const int rg = r0 + lane;
+    const int64_t t = rg < ng ? (int64_t)g.Hkv * (KO + group_tiles<R, T>(c.s, G, rg, a.causal)) : 0;
+    const int l = find_lane(t, base, x);
+    if (l >= 0) {
       c.rg = r0 + l;
       break;
     }
-    base += __shfl_sync(0xffffffffu, v, 31);
   }
   c.nt = group_tiles<R, T>(c.s, G, c.rg, a.causal);
-  c.h = (int)((x - base) / c.nt);
-  c.u0 = base + (int64_t)c.h * c.nt;
+  c.h = (int)((x - base) / (KO + c.nt));
+  c.u0 = base + (int64_t)c.h * (KO + c.nt);
   return c;
 }
 
 // The next unit of the list (the caller knows that there is one).
-template <int R, int T>
+template <int R, int T, int KO>
 __device__ __forceinline__ void next_unit(const PGeom& g, const PagedAttn& a, int G, Cursor& c) {
-  c.u0 += c.nt;
+  c.u0 += KO + c.nt;
   if (++c.h < g.Hkv) return;
   c.h = 0;
   if (++c.rg >= seq_groups<R>(c.s, G)) {
@@ -161,8 +194,20 @@ __device__ __forceinline__ void next_unit(const PGeom& g, const PagedAttn& a, in
   c.nt = group_tiles<R, T>(c.s, G, c.rg, a.causal);
 }
 
-// CTAs that take part in W tiles (at least `least` tiles each), the first tile of CTA c, and
-// the CTA that holds tile x.
+// The tiles [first, last) of a unit in a share [x0, x1) of the list, and the CTAs that hold its tiles.
+template <int KO>
+struct Segment {
+  int first, last;
+  __device__ __forceinline__ Segment(const Cursor& c, int64_t x0, int64_t x1) {
+    first = (int)max((int64_t)0, x0 - c.u0 - KO);
+    last = (int)max((int64_t)0, min(x1 - c.u0, (int64_t)KO + c.nt) - KO);
+  }
+  __device__ __forceinline__ bool empty() const { return last <= first; }
+  __device__ __forceinline__ bool whole(const Cursor& c) const { return first == 0 && last == c.nt; }
+};
+
+// CTAs that take part in W places (at least `least` each), the first place of CTA c, and the CTA
+// that holds place x.
 __device__ __forceinline__ int64_t share_ctas(int64_t W, int ctas, int least) {
   return max((int64_t)1, min((int64_t)ctas, (W + least - 1) / least));
 }
