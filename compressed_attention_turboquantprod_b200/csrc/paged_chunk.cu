@@ -140,6 +140,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
       : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Wait for the tensor-memory loads of this thread, tied to the registers they fill, so that no use
 // of those is moved before it.
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
@@ -224,11 +230,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
   const uint32_t tmem = sh.tmem;
   Cursor cur = sh.cur;
   auto wait = [&](uint64_t* bar, int index) {         // completion `index` (0, 1, ...) of a barrier
-    if (*static_cast<volatile int*>(&sh.abort)) return;
-    if (!mbar_wait_timed(bar, (uint32_t)(index & 1))) {
-      sh.abort = 1;
-      atomicOr(&g.state->status, kPagedWait);
-    }
+    if (!mbar_wait_timed(bar, (uint32_t)(index & 1), &sh.abort)) atomicOr(&g.state->status, kPagedWait);
   };
   // Each role walks the CTA's units by itself: f(tiles of the unit in this CTA's share, how many of
   // them are to be worked on (none in a unit that sees nothing), such tiles before, segments with such tiles before).
@@ -435,31 +437,40 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       if (nt > 0) {
         // ---- the warp's 32 query rows into the A operand: the largest entry of a row into [2^14,
         // 2^15) by a power of two; a negative scale turns the row's sign
-#pragma unroll 4
-        for (int i = 0; i < 32 / RI; ++i) {
-          const int rr = 32 * w4 + i * RI + lane / RL, c = lane % RL;
-          const int64_t at = place(128 * wg + rr, a.q_stride);
-          const uint4 q = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + at)[c] : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-          float mx = 0.f;
+        constexpr int BI = 32 / RI < 8 ? 32 / RI : 8;  // reads in flight (a store between them would hold them up)
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32 / RI; i0 += BI) {
+          const int c = lane % RL;
+          uint4 q[BI];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 v = unpack2(w[k], f16);
-            const float t0 = fabsf(v.x), t1 = fabsf(v.y);
-            mx = fmaxf(mx, fmaxf(t0 <= 3.402823466e38f ? t0 : 0.f, t1 <= 3.402823466e38f ? t1 : 0.f));
+          for (int i = 0; i < BI; ++i) {
+            const int64_t at = place(128 * wg + 32 * w4 + (i0 + i) * RI + lane / RL, a.q_stride);
+            q[i] = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + at)[c] : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
-          for (int o = RL / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const int e = min(mx > 0.f ? 141 - (int)(__float_as_uint(mx) >> 23) : 0, 120);
-          const float up = copysignf(__int_as_float((127 + e) << 23), a.scale);
-          uint32_t o[4];
+          for (int i = 0; i < BI; ++i) {
+            const int rr = 32 * w4 + (i0 + i) * RI + lane / RL;
+            const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+            float mx = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 v = unpack2(w[k], f16);
-            o[k] = pack_half(v.x * up, v.y * up);
+            for (int k = 0; k < 4; ++k) {
+              const float2 v = unpack2(w[k], f16);
+              const float t0 = fabsf(v.x), t1 = fabsf(v.y);
+              mx = fmaxf(mx, fmaxf(t0 <= 3.402823466e38f ? t0 : 0.f, t1 <= 3.402823466e38f ? t1 : 0.f));
+            }
+#pragma unroll
+            for (int o = RL / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int e = min(mx > 0.f ? 141 - (int)(__float_as_uint(mx) >> 23) : 0, 120);
+            const float up = copysignf(__int_as_float((127 + e) << 23), a.scale);
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 v = unpack2(w[k], f16);
+              o[k] = pack_half(v.x * up, v.y * up);
+            }
+            *reinterpret_cast<uint4*>(Q + sw_off<128>(rr, c)) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (c == 0) sh.fr[128 * wg + rr] = fabsf(a.scale) * kLog2e * __int_as_float((127 - e) << 23);
           }
-          *reinterpret_cast<uint4*>(Q + sw_off<128>(rr, c)) = make_uint4(o[0], o[1], o[2], o[3]);
-          if (c == 0) sh.fr[128 * wg + rr] = fabsf(a.scale) * kLog2e * __int_as_float((127 - e) << 23);
         }
         tc::fence_async_shared();
         tc::fence_before_sync();
@@ -497,9 +508,9 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         for (int h = 0; h < T / 16; ++h) {
           f[h] = fr * sh.sk[sc][h];
           lv[h] = sh.lv[sc][h];
-          float m = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) m = fmaxf(m, __uint_as_float(v[h >> 1][16 * (h & 1) + i]));
+          auto S = [&](int i) { return __uint_as_float(v[h >> 1][16 * (h & 1) + i]); };
+          const float m = max3(max3(max3(S(0), S(1), S(2)), max3(S(3), S(4), S(5)), max3(S(6), S(7), S(8))),
+                               max3(max3(S(9), S(10), S(11)), S(12), S(13)), fmaxf(S(14), S(15)));
           zmax = fmaxf(zmax, m == -INFINITY ? m : fmaf(m, f[h], lv[h]));
         }
         if (__any_sync(0xffffffffu, M == kNone ? zmax > -INFINITY : zmax > M + kSlack)) {

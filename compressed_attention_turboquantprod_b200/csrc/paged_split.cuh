@@ -214,21 +214,33 @@ __device__ __forceinline__ int64_t share_ctas(int64_t W, int ctas, int least) {
 __device__ __forceinline__ int64_t share_begin(int64_t W, int64_t C, int64_t c) { return W * c / C; }
 __device__ __forceinline__ int share_owner(int64_t W, int64_t C, int64_t x) { return (int)(((x + 1) * C - 1) / W); }
 
-// Wait on phase `parity` of an mbarrier for at most 2^31 cycles (about a second).
-__device__ __forceinline__ bool mbar_wait_timed(uint64_t* bar, uint32_t parity) {
-  const uint32_t a = smem_u32(bar);
+// Whether phase `parity` of an mbarrier is complete (the thread may sleep a little for it).
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Wait on phase `parity` for at most 2^31 cycles (about a second); once a wait of the CTA has given
+// up (*abort), none waits any more.
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, int* abort) {
   const long long t0 = clock64();
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (clock64() - t0 > (1ll << 31)) return false;
+  while (!mbar_try(bar, parity)) {
+    if (*static_cast<volatile int*>(abort)) return true;
+    if (clock64() - t0 > (1ll << 31)) {
+      *static_cast<volatile int*>(abort) = 1;
+      return false;
+    }
   }
+  return true;
+}
+// The same with the usual case, a completed phase, inline (a clock read costs more than the test).
+__device__ __forceinline__ bool mbar_wait_timed(uint64_t* bar, uint32_t parity, int* abort) {
+  return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, abort);
 }
 
 __device__ __forceinline__ float ex2(float x) {
