@@ -7,10 +7,10 @@
 //   P_w = 2^(f S_w + log2 s_v - M)      a thread per row, f16 back into tensor memory over S_w
 //   O_w += P_w V        A = P_w (tensor memory), B = V (D x T, shared memory)
 // A warpgroup per row block runs its softmax, four converter warps read the next tile's codes
-// into registers while they expand the last one's into the f16 operands, and one warp issues the
-// products.  The products of one row block run while the other's softmax does; with MT = 1 two S
-// buffers take their place.  The roles meet at mbarriers only, so that converters run ahead into the
-// next unit while the softmax warps finish the last.
+// into registers while they expand the last one's into the f16 operands, three warps bring the next
+// unit's queries, and one warp issues the products: Q K^T a tile ahead of P V, so that S of the next
+// tile is there when a softmax has finished one.  The roles meet at mbarriers only: converters, queries
+// and the first Q K^T run ahead into the next unit while the softmax warps write out the last.
 //
 // The scales enter exactly and at no cost per element: a page's key scale multiplies the row's
 // factor f (one per 16 tokens), its value scale is added to the exponent, so that O sums code
@@ -29,17 +29,21 @@ using namespace paged;
 
 constexpr int kChunkCtas = 148;
 constexpr int kConv = 4;                   // converter warps
+constexpr int kLoad = 3;                   // query warps
 constexpr float kNone = -1e30f;            // reference of a row that has seen no token
 constexpr float kBias = 11.f;              // p is held times 2^11
 constexpr float kSlack = 4.f;
 
 constexpr int kTokens = 64;                // tokens of a tile
-constexpr int kUnitCost = 4;               // places of a unit besides its tiles
+constexpr int kUnitCost = 8;               // places of a unit besides its tiles (16k cycles, 2k a tile)
 template <int D>
 __host__ __device__ constexpr int chunk_max_mt() { return D == 256 ? 1 : 2; }
+// Query operands: this unit's and the next one's, where they fit.
+template <int D>
+__host__ __device__ constexpr int chunk_q_bufs() { return D == 256 ? 1 : 2; }
 template <int D, int MT>
 __host__ __device__ constexpr size_t chunk_smem() {
-  return 1024 + (size_t)MT * 128 * D * 2 + 4 * (size_t)kTokens * D * 2;
+  return 1024 + (size_t)chunk_q_bufs<D>() * MT * 128 * D * 2 + 4 * (size_t)kTokens * D * 2;
 }
 
 // Operands lie in shared memory K-major in the 128-byte swizzle: slabs of 64 f16 along K, a row
@@ -111,11 +115,11 @@ __device__ __forceinline__ ChunkWs chunk_ws(void* ws) {
 
 template <int MT>
 struct ChunkShared {
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], scales[4];
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], q_free[2], o_free[2], scales[4];
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];      // [row block][tile mod 2]
   SplitPlan plan;
   float sk[4][4], lv[4][4];                // a tile's scales per 16 tokens: of the keys, log2 of the values'
-  float fr[128 * MT];                      // a row's factor on S
+  float fr[2][128 * MT];                   // a row's factor on S, per query operand
   Cursor cur;
   uint32_t tmem;
   int abort, last[2];
@@ -183,8 +187,10 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);       // known to be the same in all lanes
   const int wg = warp >> 2;                           // < MT: softmax of row block wg
-  const bool is_soft = wg < MT, is_conv = wg == MT, is_mma = warp == 4 * MT + kConv;   // the other three warps rest
-  const uint32_t sQ = smem_u32(smem), sK = sQ + R * D * 2, sV = sK + 2 * kTb;
+  const bool is_soft = wg < MT, is_conv = wg == MT, is_mma = warp == 4 * MT + kConv;
+  constexpr int NQ = chunk_q_bufs<D>();
+  constexpr uint32_t kQb = R * D * 2;                 // bytes of a query operand
+  const uint32_t sQ = smem_u32(smem), sK = sQ + NQ * kQb, sV = sK + 2 * kTb;
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) mbar_init(&sh.scales[i], kConv);
     for (int i = 0; i < 2; ++i) {
@@ -192,7 +198,9 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       mbar_init(&sh.k_free[i], 1);
       mbar_init(&sh.v_full[i], kConv);
       mbar_init(&sh.v_free[i], 1);
-      mbar_init(&sh.q_full[i], 4);
+      mbar_init(&sh.q_full[i], kLoad);
+      mbar_init(&sh.q_free[i], 4 * MT);
+      mbar_init(&sh.o_free[i], 4);
       for (int w = 0; w < 2; ++w) {
         mbar_init(&sh.s_full[w][i], 1);
         mbar_init(&sh.p_ready[w][i], 4);
@@ -249,6 +257,21 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       if (x < x1) next_unit<R, T, kUnitCost>(g, a, G, cur);
     }
   };
+
+  // row / G for row < 2^27, G <= 8: the reciprocal's error times row stays below 1 / G
+  const uint32_t gm = (uint32_t)(0x100000000ull / (uint32_t)G) + 1u;
+  auto by_g = [&](int row) { return G == 1 ? row : (int)__umulhi((uint32_t)row, gm); };
+  // Place of row i of the unit in an array of tokens `stride` entries apart (a token's heads lie side
+  // by side), in entries; -1: none.
+  auto place = [&](int i, int64_t stride) {
+    const int row0 = cur.rg * R, q = by_g(row0 + i);
+    const int64_t tok = (int64_t)cur.s.q0 + q;
+    return row0 + i < cur.s.nq * G && i < R && tok >= 0 && tok < a.total_q
+               ? tok * stride + (cur.h * G + row0 + i - q * G) * D
+               : (int64_t)-1;
+  };
+  // rows of D / 8 16-byte pieces: RL lanes a row, RI rows an instruction
+  constexpr int RL = D / 8, RI = 32 / RL;
 
   if (is_conv) {
     // =================================================================== converters
@@ -327,7 +350,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       if (nt > 1) look(1);
       for (int t = 0; t < nt; ++t) {
         const int n = n0 + t, b2 = n & 1;
-        unsigned char* K = smem + R * D * 2 + b2 * kTb;
+        unsigned char* K = smem + NQ * kQb + b2 * kTb;
         unsigned char* V = K + 2 * kTb;
         if (n >= 2) wait(&sh.k_free[b2], (n >> 1) - 1);
         // four sets of scales: the products of tile n - 2 are done, so the softmax of tile n - 4 is
@@ -363,10 +386,10 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dQ = sw_desc(__shfl_sync(0xffffffffu, sQ, 0)), dK = sw_desc(__shfl_sync(0xffffffffu, sK, 0)),
                    dV = sw_desc(__shfl_sync(0xffffffffu, sV, 0));
-    auto qk = [&](int w, int b2) {
+    auto qk = [&](int w, int b2, int qb) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
-        mma_ss(tm + cS + (2 * w + b2) * T, dQ + (uint64_t)(w * (128 * D * 2 / 16) + sw_step<128>(k)),
+        mma_ss(tm + cS + (2 * w + b2) * T, dQ + (uint64_t)(qb * (kQb / 16) + w * (128 * D * 2 / 16) + sw_step<128>(k)),
                dK + (uint64_t)(b2 * (kTb / 16) + sw_step<T>(k)), iS, k > 0);
     };
     auto pv = [&](int w, int b2, bool first) {
@@ -382,15 +405,14 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       for (int t = -1; t < nt; ++t) {
         const int n = n0 + t, m = n + 1;
         if (t + 1 < nt) {
+          if (t < 0) wait(&sh.q_full[seg % NQ], seg / NQ);
           wait(&sh.k_full[m & 1], m >> 1);
 #pragma unroll
           for (int w = 0; w < MT; ++w) {
-            // the row block's queries are in place and its last unit's O has been read; or P of tile
-            // n - 1, over this S buffer, has been used
-            if (t < 0) wait(&sh.q_full[w], seg);
-            if (t >= 1) wait(&sh.pv_done[w][m & 1], (n - 1) >> 1);
+            // P of tile n - 1, over this S buffer, has been used (in the first tiles of a unit, too)
+            if (n >= 1) wait(&sh.pv_done[w][m & 1], (n - 1) >> 1);
             tc::fence_after_sync();
-            qk(w, m & 1);
+            qk(w, m & 1, seg % NQ);
             mma_commit_elected(&sh.s_full[w][m & 1]);
           }
           mma_commit_elected(&sh.k_free[m & 1]);
@@ -400,6 +422,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
 #pragma unroll
           for (int w = 0; w < MT; ++w) {
             wait(&sh.p_ready[w][n & 1], n >> 1);
+            if (t == 0 && seg > 0) wait(&sh.o_free[w], seg - 1);      // the last unit's O has been read
             tc::fence_after_sync();
             pv(w, n & 1, t == 0);
             mma_commit_elected(&sh.pv_done[w][n & 1]);
@@ -414,69 +437,17 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
     const uint32_t tO = tmem + lrow + cO + wg * D;
     const bool f16 = g.dtype == TQ_F16;
     const int w4 = warp & 3, r = tid;                  // this thread's row of the CTA's
-    unsigned char* Q = smem + (size_t)wg * 128 * D * 2;  // the row block's operand, later its output
     const ChunkWs ws = chunk_ws<D, MT>(a.ws);
-    // row / G for row < 2^27, G <= 8: the reciprocal's error times row stays below 1 / G
-    const uint32_t gm = (uint32_t)(0x100000000ull / (uint32_t)G) + 1u;
-    auto by_g = [&](int row) { return G == 1 ? row : (int)__umulhi((uint32_t)row, gm); };
-    // rows of D / 8 16-byte pieces: RL lanes a row, RI rows an instruction
-    constexpr int RL = D / 8, RI = 32 / RL;
-    walk([&](const auto& sg, int nt, int n0, int) {
+    walk([&](const auto& sg, int nt, int n0, int seg) {
       const int tok0 = sg.first * T;                   // the segment's first token
-      const int rows = (int)min((int64_t)R, (int64_t)cur.s.nq * G - (int64_t)cur.rg * R);
       const int row0 = cur.rg * R;                     // the CTA's first row of the sequence (below 2^27)
-      // place of CTA row i's D entries in Q and out (heads of a token lie side by side); -1: none
-      auto place = [&](int i, int64_t stride) {
-        const int q = by_g(row0 + i);
-        const int64_t tok = (int64_t)cur.s.q0 + q;
-        return i < rows && tok >= 0 && tok < a.total_q ? tok * stride + (cur.h * G + row0 + i - q * G) * D : (int64_t)-1;
-      };
       const bool ok = place(r, 0) >= 0;
       const int vis = ok ? visible(cur.s, by_g(row0 + r), a.causal) : 0;
       float fr = 0.f, M = kNone, l = 0.f, lvr = 0.f;
+      unsigned char* Q = smem + (seg % NQ) * kQb + (size_t)wg * 128 * D * 2;  // the row block's operand, later its output
       if (nt > 0) {
-        // ---- the warp's 32 query rows into the A operand: the largest entry of a row into [2^14,
-        // 2^15) by a power of two; a negative scale turns the row's sign
-        constexpr int BI = 32 / RI < 8 ? 32 / RI : 8;  // reads in flight (a store between them would hold them up)
-#pragma unroll 1
-        for (int i0 = 0; i0 < 32 / RI; i0 += BI) {
-          const int c = lane % RL;
-          uint4 q[BI];
-#pragma unroll
-          for (int i = 0; i < BI; ++i) {
-            const int64_t at = place(128 * wg + 32 * w4 + (i0 + i) * RI + lane / RL, a.q_stride);
-            q[i] = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + at)[c] : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int i = 0; i < BI; ++i) {
-            const int rr = 32 * w4 + (i0 + i) * RI + lane / RL;
-            const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-            float mx = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 v = unpack2(w[k], f16);
-              const float t0 = fabsf(v.x), t1 = fabsf(v.y);
-              mx = fmaxf(mx, fmaxf(t0 <= 3.402823466e38f ? t0 : 0.f, t1 <= 3.402823466e38f ? t1 : 0.f));
-            }
-#pragma unroll
-            for (int o = RL / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const int e = min(mx > 0.f ? 141 - (int)(__float_as_uint(mx) >> 23) : 0, 120);
-            const float up = copysignf(__int_as_float((127 + e) << 23), a.scale);
-            uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 v = unpack2(w[k], f16);
-              o[k] = pack_half(v.x * up, v.y * up);
-            }
-            *reinterpret_cast<uint4*>(Q + sw_off<128>(rr, c)) = make_uint4(o[0], o[1], o[2], o[3]);
-            if (c == 0) sh.fr[128 * wg + rr] = fabsf(a.scale) * kLog2e * __int_as_float((127 - e) << 23);
-          }
-        }
-        tc::fence_async_shared();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.q_full[wg]);
-        fr = ok ? sh.fr[r] : 0.f;
+        wait(&sh.q_full[seg % NQ], seg / NQ);
+        fr = ok ? sh.fr[seg % NQ][r] : 0.f;
       }
       // A parity tells a completion only from its neighbours, so every waiter has to be within one of
       // it: S of tile n came after P V of n - 2 only, hence a barrier per buffer.
@@ -576,19 +547,17 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         for (int i = 0; i < 32 / RI; ++i) {
           const int rr = 32 * w4 + i * RI + lane / RL, c = lane % RL;
           const int64_t at = place(128 * wg + rr, (int64_t)a.Hq * D);
-          const uint4 v = *reinterpret_cast<const uint4*>(Q + sw_off<128>(rr, c));
+          const uint4 v = nt > 0 ? *reinterpret_cast<const uint4*>(Q + sw_off<128>(rr, c)) : make_uint4(0, 0, 0, 0);
           if (at >= 0) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at)[c] = v;
         }
         __syncwarp();
       };
       float4* part = reinterpret_cast<float4*>(ws.o + (int64_t)slot * R * D) + r;      // [D / 4][R]
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < D / 32 && nt > 0; ++c) {
         uint32_t v[32];
-        if (nt > 0) {
-          tc::tmem_ld32(tO + 32 * c, v);
-          tmem_wait_ld(v);
-        }
+        tc::tmem_ld32(tO + 32 * c, v);
+        tmem_wait_ld(v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float o[8];
@@ -602,6 +571,11 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
             part[(int64_t)(8 * c + 2 * i + 1) * R] = make_float4(o[4], o[5], o[6], o[7]);
           }
         }
+      }
+      if (nt > 0) {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.o_free[wg]);
       }
       if (whole) {
         rows_out();
@@ -658,7 +632,59 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
                 L > 0.f ? (m + log2f(L)) * (1.f / kLog2e) : -INFINITY;
         }
       }
-      tc::fence_before_sync();
+      if (nt > 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_free[seg % NQ]);
+      }
+    });
+  } else {
+    // =================================================================== queries
+    // The unit's rows into the A operand: the largest entry of a row into [2^14, 2^15) by a power of
+    // two; a negative scale turns the row's sign.
+    const bool f16 = g.dtype == TQ_F16;
+    const int lw = warp - (4 * MT + kConv + 1);
+    walk([&](const auto&, int nt, int, int seg) {
+      if (nt == 0) return;
+      const int qb = seg % NQ;
+      if (seg >= NQ) wait(&sh.q_free[qb], seg / NQ - 1);
+      constexpr int BI = 8;                            // reads in flight (a store between them would hold them up)
+      const int c = lane % RL;
+#pragma unroll 1
+      for (int i0 = lw * BI; i0 < R / RI; i0 += kLoad * BI) {
+        uint4 q[BI];
+#pragma unroll
+        for (int i = 0; i < BI; ++i) {
+          const int64_t at = place((i0 + i) * RI + lane / RL, a.q_stride);
+          q[i] = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + at)[c] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < BI; ++i) {
+          const int rr = (i0 + i) * RI + lane / RL;
+          const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+          // |entries| compare as integers in both types (a NaN or infinity spoils its own row only)
+          uint32_t m2 = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m2 = __vmaxu2(m2, w[k] & 0x7fff7fffu);
+          uint32_t m1 = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+          for (int o = RL / 2; o > 0; o >>= 1) m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+          const float mx = unpack2(m1, f16).x;
+          const int e = min(mx > 0.f ? 141 - (int)(__float_as_uint(mx) >> 23) : 0, 120);
+          const float up = copysignf(__int_as_float((127 + e) << 23), a.scale);
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = unpack2(w[k], f16);
+            o[k] = pack_half(v.x * up, v.y * up);
+          }
+          *reinterpret_cast<uint4*>(smem + qb * kQb + (rr >> 7) * (128 * D * 2) + sw_off<128>(rr & 127, c)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+          if (c == 0) sh.fr[qb][rr] = fabsf(a.scale) * kLog2e * __int_as_float((127 - e) << 23);
+        }
+      }
+      tc::fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full[qb]);
     });
   }
   __syncthreads();
