@@ -115,7 +115,7 @@ __device__ __forceinline__ ChunkWs chunk_ws(void* ws) {
 
 template <int MT>
 struct ChunkShared {
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], q_free[2], o_free[2], scales[4];
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], q_free[2], o_free[2];
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];      // [row block][tile mod 2]
   SplitPlan plan;
   float sk[4][4], lv[4][4];                // a tile's scales per 16 tokens: of the keys, log2 of the values'
@@ -192,7 +192,6 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
   constexpr uint32_t kQb = R * D * 2;                 // bytes of a query operand
   const uint32_t sQ = smem_u32(smem), sK = sQ + NQ * kQb, sV = sK + 2 * kTb;
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.scales[i], kConv);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.k_full[i], kConv);
       mbar_init(&sh.k_free[i], 1);
@@ -202,7 +201,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       mbar_init(&sh.q_free[i], 4 * MT);
       mbar_init(&sh.o_free[i], 4);
       for (int w = 0; w < 2; ++w) {
-        mbar_init(&sh.s_full[w][i], 1);
+        mbar_init(&sh.s_full[w][i], 2);       // the products, and the warp that saw the tile's scales
         mbar_init(&sh.p_ready[w][i], 4);
         mbar_init(&sh.pv_done[w][i], 1);
       }
@@ -272,6 +271,47 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
   };
   // rows of D / 8 16-byte pieces: RL lanes a row, RI rows an instruction
   constexpr int RL = D / 8, RI = 32 / RL;
+
+  // The unit's rows into query operand qb, by warp w of nw: the largest entry of a row into [2^14,
+  // 2^15) by a power of two; a negative scale turns the row's sign.
+  const bool f16 = g.dtype == TQ_F16;
+  auto bring_queries = [&](int qb, int w, int nw) {
+    constexpr int BI = 8;                            // reads in flight (a store between them would hold them up)
+    const int c = lane % RL;
+#pragma unroll 1
+    for (int i0 = w * BI; i0 < R / RI; i0 += nw * BI) {
+      uint4 q[BI];
+#pragma unroll
+      for (int i = 0; i < BI; ++i) {
+        const int64_t at = place((i0 + i) * RI + lane / RL, a.q_stride);
+        q[i] = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + at)[c] : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < BI; ++i) {
+        const int rr = (i0 + i) * RI + lane / RL;
+        const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+        // |entries| compare as integers in both types (a NaN or infinity spoils its own row only)
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m2 = __vmaxu2(m2, u[k] & 0x7fff7fffu);
+        uint32_t m1 = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+        for (int o = RL / 2; o > 0; o >>= 1) m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+        const float mx = unpack2(m1, f16).x;
+        const int e = min(mx > 0.f ? 141 - (int)(__float_as_uint(mx) >> 23) : 0, 120);
+        const float up = copysignf(__int_as_float((127 + e) << 23), a.scale);
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = unpack2(u[k], f16);
+          o[k] = pack_half(v.x * up, v.y * up);
+        }
+        *reinterpret_cast<uint4*>(smem + qb * kQb + (rr >> 7) * (128 * D * 2) + sw_off<128>(rr & 127, c)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+        if (c == 0) sh.fr[qb][rr] = fabsf(a.scale) * kLog2e * __int_as_float((127 - e) << 23);
+      }
+    }
+  };
 
   if (is_conv) {
     // =================================================================== converters
@@ -358,8 +398,6 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
           sh.sk[n & 3][cw * NH + lane] = sk;
           sh.lv[n & 3][cw * NH + lane] = sv > 0.f ? __log2f(sv) : 0.f;     // a block of zeros: any scale will do
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.scales[n & 3]);
 #pragma unroll
         for (int it = 0; it < NK; ++it) {
           unsigned char* to = K + (it % (D / 64)) * (T * 128) + (it / (D / 64)) * 1024;
@@ -414,6 +452,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
             tc::fence_after_sync();
             qk(w, m & 1, seg % NQ);
             mma_commit_elected(&sh.s_full[w][m & 1]);
+            if (lane == 0) mbar_arrive(&sh.s_full[w][m & 1]);
           }
           mma_commit_elected(&sh.k_free[m & 1]);
         }
@@ -435,7 +474,6 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
     // =================================================================== softmax
     const uint32_t lrow = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tO = tmem + lrow + cO + wg * D;
-    const bool f16 = g.dtype == TQ_F16;
     const int w4 = warp & 3, r = tid;                  // this thread's row of the CTA's
     const ChunkWs ws = chunk_ws<D, MT>(a.ws);
     walk([&](const auto& sg, int nt, int n0, int seg) {
@@ -446,6 +484,12 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       float fr = 0.f, M = kNone, l = 0.f, lvr = 0.f;
       unsigned char* Q = smem + (seg % NQ) * kQb + (size_t)wg * 128 * D * 2;  // the row block's operand, later its output
       if (nt > 0) {
+        if (seg == 0) {
+          bring_queries(0, warp, 4 * MT);
+          tc::fence_async_shared();
+          tc::bar_sync(3, 128 * MT);
+          if (lane == 0 && warp < kLoad) mbar_arrive(&sh.q_full[0]);
+        }
         wait(&sh.q_full[seg % NQ], seg / NQ);
         fr = ok ? sh.fr[seg % NQ][r] : 0.f;
       }
@@ -454,19 +498,31 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       auto pv_wait = [&](int n) { wait(&sh.pv_done[wg][n & 1], n >> 1); };
       // the rows of the warp see at least wmin tokens
       const int wmin = __reduce_min_sync(0xffffffffu, vis);
+      // S of the next tile is requested as the registers of this one's halves come free, and P is
+      // handed over when the next tile's work has begun: neither latency is waited for
+      uint32_t v[2][32];                               // the row of S
+      auto s_at = [&](int n) { return tmem + lrow + cS + (2 * wg + (n & 1)) * T; };
+      auto hand_over = [&](int n) {                    // P of tile n is in place
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        // (a warp may finish tile n + 1 before another has finished n, but not n + 2)
+        if (lane == 0) mbar_arrive(&sh.p_ready[wg][n & 1]);
+      };
+      if (nt > 0) {
+        wait(&sh.s_full[wg][n0 & 1], n0 >> 1);
+        tc::fence_after_sync();
+        lvr = sh.lv[n0 & 3][0];
+        tc::tmem_ld32(s_at(n0), v[0]);
+        tc::tmem_ld32(s_at(n0) + 32, v[1]);
+      }
       for (int t = 0; t < nt; ++t) {
         const int n = n0 + t, sc = n & 3;
-        const uint32_t tS = tmem + lrow + cS + (2 * wg + (n & 1)) * T;
+        const uint32_t tS = s_at(n);
         const int base = tok0 + t * T;                 // the tile's first token
-        wait(&sh.scales[sc], n >> 2);
-        wait(&sh.s_full[wg][n & 1], n >> 1);
-        tc::fence_after_sync();
-        if (t == 0) lvr = sh.lv[sc][0];
-        uint32_t v[2][32];                             // the row of S
-        tc::tmem_ld32(tS, v[0]);
-        tc::tmem_ld32(tS + 32, v[1]);
         tmem_wait_ld(v[0]);
         tmem_wait_ld(v[1]);
+        if (t > 0) hand_over(n - 1);
         if (base + T > wmin) {                         // a tile that not every row of the warp sees in full
 #pragma unroll
           for (int c = 0; c < 2; ++c)
@@ -523,13 +579,16 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
             l = fmaf(ls.x + ls.y, ex2(lvr - lv[h]), l);
           }
           tmem_st16(tS + 16 * c, pk);
+          if (t + 1 < nt) {
+            if (c == 0) {
+              wait(&sh.s_full[wg][(n + 1) & 1], (n + 1) >> 1);
+              tc::fence_after_sync();
+            }
+            tc::tmem_ld32(s_at(n + 1) + 32 * c, v[c]);
+          }
         }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        // (a warp may finish tile n + 1 before another has finished n, but not n + 2)
-        if (lane == 0) mbar_arrive(&sh.p_ready[wg][n & 1]);
       }
+      if (nt > 0) hand_over(n0 + nt - 1);
       // ---- the row's output, or its part
       const bool whole = sg.whole(cur);
       const float inv = l > 0.f ? ex2(lvr) / l : 0.f;
@@ -639,49 +698,13 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
     });
   } else {
     // =================================================================== queries
-    // The unit's rows into the A operand: the largest entry of a row into [2^14, 2^15) by a power of
-    // two; a negative scale turns the row's sign.
-    const bool f16 = g.dtype == TQ_F16;
+    // the first unit's come from the softmax warps, which would only wait for them
     const int lw = warp - (4 * MT + kConv + 1);
     walk([&](const auto&, int nt, int, int seg) {
-      if (nt == 0) return;
+      if (nt == 0 || seg == 0) return;
       const int qb = seg % NQ;
       if (seg >= NQ) wait(&sh.q_free[qb], seg / NQ - 1);
-      constexpr int BI = 8;                            // reads in flight (a store between them would hold them up)
-      const int c = lane % RL;
-#pragma unroll 1
-      for (int i0 = lw * BI; i0 < R / RI; i0 += kLoad * BI) {
-        uint4 q[BI];
-#pragma unroll
-        for (int i = 0; i < BI; ++i) {
-          const int64_t at = place((i0 + i) * RI + lane / RL, a.q_stride);
-          q[i] = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + at)[c] : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < BI; ++i) {
-          const int rr = (i0 + i) * RI + lane / RL;
-          const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-          // |entries| compare as integers in both types (a NaN or infinity spoils its own row only)
-          uint32_t m2 = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m2 = __vmaxu2(m2, w[k] & 0x7fff7fffu);
-          uint32_t m1 = max(m2 & 0xffffu, m2 >> 16);
-#pragma unroll
-          for (int o = RL / 2; o > 0; o >>= 1) m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-          const float mx = unpack2(m1, f16).x;
-          const int e = min(mx > 0.f ? 141 - (int)(__float_as_uint(mx) >> 23) : 0, 120);
-          const float up = copysignf(__int_as_float((127 + e) << 23), a.scale);
-          uint32_t o[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 v = unpack2(w[k], f16);
-            o[k] = pack_half(v.x * up, v.y * up);
-          }
-          *reinterpret_cast<uint4*>(smem + qb * kQb + (rr >> 7) * (128 * D * 2) + sw_off<128>(rr & 127, c)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-          if (c == 0) sh.fr[qb][rr] = fabsf(a.scale) * kLog2e * __int_as_float((127 - e) << 23);
-        }
-      }
+      bring_queries(qb, lw, kLoad);
       tc::fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full[qb]);

@@ -227,7 +227,7 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
 }
 // Wait on phase `parity` for at most 2^31 cycles (about a second); once a wait of the CTA has given
 // up (*abort), none waits any more.
-static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, int* abort) {
+__device__ __forceinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, int* abort) {
   const long long t0 = clock64();
   while (!mbar_try(bar, parity)) {
     if (*static_cast<volatile int*>(abort)) return true;
