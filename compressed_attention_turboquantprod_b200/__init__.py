@@ -8,6 +8,7 @@ exists); using any class here without a built ``libtq.so`` raises ImportError.
 """
 from __future__ import annotations
 
+import contextlib
 import importlib
 import math
 from typing import Optional
@@ -206,6 +207,9 @@ class CompressedKVCache:
         return (out, logits) if want_logits else out
 
 
+_CURRENT = contextlib.nullcontext()       # a call on the current device needs no switch
+
+
 class PagedKVCache:
     """Keys and values in 8 bits, in pages of `page` tokens with one scale per page and KV head;
     sequences of any lengths, named by slots 0 .. slots-1, that fork, copy and free.
@@ -227,16 +231,20 @@ class PagedKVCache:
         if nbytes == 0:
             native.tq_paged_layout(self.desc)      # raises with the reason
         self.buffer = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self._index = self.buffer.device.index
         self.state = native.tq_paged()
         with torch.cuda.device(self.buffer.device):
             native.tq_paged_init(self.state, self.desc, self.buffer)
         self._ws = {}
+        self._cu = {}
 
     def _on(self, *tensors):
         """The cache's device made current; every tensor of the call has to be on it."""
         for t in tensors:
             if t is not None and t.device != self.buffer.device:
                 raise ValueError(f"tensor on {t.device}, the cache is on {self.buffer.device}")
+        if torch.cuda.current_device() == self._index:
+            return _CURRENT
         return torch.cuda.device(self.buffer.device)
 
     def _typed(self, *tensors):
@@ -250,7 +258,7 @@ class PagedKVCache:
         ready by the graph itself."""
         if torch.cuda.is_current_stream_capturing():
             return self.make_workspace()
-        key = torch.cuda.current_stream(self.buffer.device).cuda_stream
+        key = native.raw_stream(self._index)
         if key not in self._ws:
             self._ws[key] = self.make_workspace()
         return self._ws[key]
@@ -316,7 +324,13 @@ class PagedKVCache:
         return out
 
     def _ones(self, n: int) -> torch.Tensor:
-        return torch.arange(n + 1, dtype=torch.int32, device=self.buffer.device)
+        """Offsets of n rows of one token, made once (in a capture: the graph's own)."""
+        if n not in self._cu:
+            if torch.cuda.is_current_stream_capturing():
+                return torch.arange(n + 1, dtype=torch.int32, device=self.buffer.device)
+            # a copy that the host waits for: there for every stream
+            self._cu[n] = torch.arange(n + 1, dtype=torch.int32).to(self.buffer.device)
+        return self._cu[n]
 
     def decode(self, Q: torch.Tensor, slots: torch.Tensor, softmax_scale: Optional[float] = None,
                layer: int = 0, cu: Optional[torch.Tensor] = None, **kw):

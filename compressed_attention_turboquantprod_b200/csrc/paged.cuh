@@ -12,6 +12,8 @@
 // one byte permutation), e4m3 codes as they are.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace tq {
@@ -85,6 +87,20 @@ __device__ __forceinline__ uint8_t* paged_tail(const PGeom& g, int layer, int sl
 // Tokens of a slot (0 for a slot out of range: callers treat it as an empty sequence).
 __device__ __forceinline__ int paged_len(const PGeom& g, int slot) {
   return (unsigned)slot < (unsigned)g.slots ? g.len[slot] : 0;
+}
+
+// The kernel's dynamic shared memory limit, set once per device and kernel.
+template <auto Kernel>
+cudaError_t paged_allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // ---- host launchers ----

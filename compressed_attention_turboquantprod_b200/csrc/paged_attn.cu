@@ -97,23 +97,36 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
   pdl_wait();
   pdl_launch_dependents();
   const int G = a.Hq / g.Hkv;
-  if (*static_cast<const volatile uint32_t*>(a.ws) != kWsMagic) {
+  const uint32_t magic = *static_cast<const volatile uint32_t*>(a.ws);
+  const int cta = blockIdx.x;
+  Cursor cur;
+  int64_t W, C = 0, x0 = 0, x1 = 0;
+  auto share = [&](int64_t w) {
+    C = share_ctas(w, gridDim.x, kDecWarps);
+    x0 = share_begin(w, C, cta);
+    x1 = share_begin(w, C, cta + 1);
+    return cta < C ? x0 : (int64_t)-1;
+  };
+  const bool few = a.n <= 32;
+  if (few) {
+    W = plan_in_warp<kDecRows, kTile, 0>(g, a, G, cur, share);
+  } else {
+    W = count_places<kDecRows, kTile, 0, kDecThreads>(g, a, G, s_plan);
+    if (W > 0) share(W);
+  }
+  if (magic != kWsMagic) {
     if (tid == 0) atomicOr(&g.state->status, kPagedBadWorkspace);
     return;
   }
   if (cta_first_checks(g, a)) atomicOr(&g.state->status, kPagedBadOffsets);
-  const int64_t W = count_places<kDecRows, kTile, 0, kDecThreads>(g, a, G, s_plan);
-  if (W == 0) return;
-  const int64_t C = share_ctas(W, gridDim.x, kDecWarps);
-  const int cta = blockIdx.x;
-  if (cta >= C) return;
-  const int64_t x0 = share_begin(W, C, cta), x1 = share_begin(W, C, cta + 1);
-  if (warp == 0) {
+  if (W == 0 || cta >= C) return;
+  if (!few && warp == 0) {
     const Cursor f = find_unit<kDecRows, kTile, 0>(g, a, G, x0, s_plan);
     if (lane == 0) s_cur = f;
   }
-  __syncthreads();
-  Cursor cur = s_cur, nxt = cur;            // the unit at work, and that of the tile to request next
+  __syncthreads();                          // the barriers are initialised, the cursor is there
+  if (!few) cur = s_cur;
+  Cursor nxt = cur;                         // the unit of the tile to request next
   const DecWs ws = dec_ws(a.ws);
 
   // ---- requests: tile x belongs to warp x mod 4; the page of the next one is read ahead
@@ -179,24 +192,37 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
     }
   };
 
+  // ---- queries: warp w brings rows 2 w and 2 w + 1 of a unit, a unit ahead
+  constexpr int NQ = D / 32;                // lane l holds channels NQ l .. NQ l + NQ - 1
+  float qn[2][NQ];
+  auto bring = [&](const Cursor& u) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = u.rg * kDecRows + 2 * warp + j;
+      const int64_t tok = (int64_t)u.s.q0 + row / G;
+      const bool ok = row < u.s.nq * G && tok >= 0 && tok < a.total_q;
+#pragma unroll
+      for (int k = 0; k < NQ; ++k)
+        qn[j][k] = ok ? load_f(a.Q, tok * a.q_stride + (int64_t)(u.h * G + row % G) * D + NQ * lane + k, g.dtype) : 0.f;
+    }
+  };
+  bring(cur);
+
   int64_t x = x0;
   while (x < x1) {
     const int64_t ue = cur.u0 + cur.nt, xe = min(x1, ue);
     // ---- the unit's queries as A fragments, two rows per warp
     __syncthreads();
     const int rows = (int)min((int64_t)kDecRows, (int64_t)cur.s.nq * G - (int64_t)cur.rg * kDecRows);
-    for (int r = 2 * warp; r < 2 * warp + 2; ++r) {
-      const int row = cur.rg * kDecRows + r;
-      const int64_t tok = (int64_t)cur.s.q0 + row / G;
-      const int hq = cur.h * G + row % G;
-      const bool ok = r < rows && tok >= 0 && tok < a.total_q;
-      constexpr int N = D / 32;
-      float q[N], mx = 0.f;
-      // lane l holds channels N l .. N l + N - 1
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        q[k] = ok ? load_f(a.Q, tok * a.q_stride + (int64_t)hq * D + N * lane + k, g.dtype) : 0.f;
-        const float t = fabsf(q[k]);
+    for (int j = 0; j < 2; ++j) {
+      const int r = 2 * warp + j, row = cur.rg * kDecRows + r;
+      const int64_t tok = (int64_t)cur.s.q0 + row / G;
+      const bool ok = r < rows && tok >= 0 && tok < a.total_q;
+      float mx = 0.f;
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) {
+        const float t = fabsf(qn[j][k]);
         mx = fmaxf(mx, t <= 3.402823466e38f ? t : 0.f);
       }
       mx = warp_max(mx);
@@ -205,11 +231,11 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
       const float up = __int_as_float((127 + e) << 23);
       __half* A = reinterpret_cast<__half*>(s_q);
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const float v = q[k] * up;
+      for (int k = 0; k < NQ; ++k) {
+        const float v = qn[j][k] * up;
         const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
         // channel 64 j + 16 c' + 4 w + b is k-step 4 j + w, lane (r, c'), register 2 (b / 2), half b mod 2
-        const int ch = N * lane + k;
+        const int ch = NQ * lane + k;
         const int ks = 4 * (ch >> 6) + ((ch >> 2) & 3), cc = (ch >> 4) & 3, b = ch & 3;
         __half* f = A + ((ks * 32 + 4 * r + cc) * 4 + 2 * (b >> 1)) * 2 + (b & 1);
         f[0] = hi;
@@ -219,6 +245,11 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
         s_fr[r] = ok ? a.scale * kLog2e * __int_as_float((127 - e) << 23) : 0.f;
         s_vis[r] = ok ? visible(cur.s, row / G, a.causal) : 0;
       }
+    }
+    if (xe < x1) {
+      Cursor after = cur;
+      next_unit<kDecRows, kTile, 0>(g, a, G, after);
+      bring(after);
     }
     __syncthreads();
     const float fr = s_fr[gi];
@@ -454,8 +485,7 @@ template <int D, int SUB, int CODE>
 cudaError_t decode_t(const PGeom& g, const PagedAttn& a, cudaStream_t s) {
   constexpr size_t smem = dec_smem<D, SUB>();
   static_assert(smem <= (DecCfg<D>::kCtas == 1 ? 226u : 113u) * 1024, "resident CTAs");
-  cudaError_t e = cudaFuncSetAttribute(k_paged_decode<D, SUB, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = paged_allow_smem<k_paged_decode<D, SUB, CODE>>(smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_paged_decode<D, SUB, CODE>, dim3(148 * DecCfg<D>::kCtas), dim3(kDecThreads), smem, s, g, a);
 }

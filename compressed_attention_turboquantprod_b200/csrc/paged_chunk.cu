@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
 template <int D, int CODE, int MT>
 cudaError_t chunk_t(const PGeom& g, const PagedAttn& a, cudaStream_t s) {
   constexpr size_t smem = chunk_smem<D, MT>();
-  cudaError_t e = cudaFuncSetAttribute(k_paged_chunk<D, CODE, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = paged_allow_smem<k_paged_chunk<D, CODE, MT>>(smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_paged_chunk<D, CODE, MT>, dim3(kChunkCtas), dim3(128 * MT + 256), smem, s, g, a);
 }

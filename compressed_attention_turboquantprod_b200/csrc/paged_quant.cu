@@ -327,8 +327,7 @@ template <typename T, int D, int CODE>
 cudaError_t write_t(const PGeom& g, int layer, const void* K, const void* V, int64_t ks, int64_t vs, int64_t total,
                     int n_rows, cudaStream_t s) {
   const size_t smem = (size_t)g.page * D * sizeof(T);
-  cudaError_t e = cudaFuncSetAttribute(k_paged_write<T, D, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = paged_allow_smem<k_paged_write<T, D, CODE>>((size_t)128 * D * sizeof(T));     // the largest page's
   if (e != cudaSuccess) return e;
   // a row of c tokens touches at most c / page + 2 pages
   const int64_t items = total / g.page + 2 * (int64_t)n_rows;

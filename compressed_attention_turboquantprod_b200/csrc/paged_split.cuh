@@ -179,6 +179,51 @@ __device__ Cursor find_unit(const PGeom& g, const PagedAttn& a, int G, int64_t x
   return c;
 }
 
+// Both at once for at most 32 sequences, by every warp for itself (one round of loads, no barrier):
+// the call's places, then, for the place that `at` makes of them, its unit (`at` < 0: none is sought).
+template <int R, int T, int KO, typename F>
+__device__ __forceinline__ int64_t plan_in_warp(const PGeom& g, const PagedAttn& a, int G, Cursor& c, F at) {
+  const int lane = threadIdx.x & 31;
+  Seq s{-1, 0, 0, 0};
+  int64_t t = 0;
+  if (lane < a.n) {
+    s = load_seq(g, a, lane);
+    const int ng = seq_groups<R>(s, G);
+    if (ng == 1 || (ng > 1 && !a.causal)) {
+      t = (int64_t)ng * (KO + group_tiles<R, T>(s, G, 0, a.causal));
+    } else {
+      for (int rg = 0; rg < ng; ++rg) t += KO + group_tiles<R, T>(s, G, rg, a.causal);
+    }
+    t *= g.Hkv;
+  }
+  int64_t W = t;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+  const int64_t x = W > 0 ? at(W) : (int64_t)-1;
+  if (x < 0) return W;
+  int64_t base = 0;
+  c.i = max(find_lane(t, base, x), 0);
+  c.s.slot = __shfl_sync(0xffffffffu, s.slot, c.i);
+  c.s.len = __shfl_sync(0xffffffffu, s.len, c.i);
+  c.s.nq = __shfl_sync(0xffffffffu, s.nq, c.i);
+  c.s.q0 = __shfl_sync(0xffffffffu, s.q0, c.i);
+  c.rg = 0;
+  const int ng = seq_groups<R>(c.s, G);
+  for (int r0 = 0; r0 < ng; r0 += 32) {
+    const int rg = r0 + lane;
+    const int64_t u = rg < ng ? (int64_t)g.Hkv * (KO + group_tiles<R, T>(c.s, G, rg, a.causal)) : 0;
+    const int l = find_lane(u, base, x);
+    if (l >= 0) {
+      c.rg = r0 + l;
+      break;
+    }
+  }
+  c.nt = group_tiles<R, T>(c.s, G, c.rg, a.causal);
+  c.h = (int)((x - base) / (KO + c.nt));
+  c.u0 = base + (int64_t)c.h * (KO + c.nt);
+  return W;
+}
+
 // The next unit of the list (the caller knows that there is one).
 template <int R, int T, int KO>
 __device__ __forceinline__ void next_unit(const PGeom& g, const PagedAttn& a, int G, Cursor& c) {

@@ -162,6 +162,20 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def raw_stream(device: int) -> int:
+    """The handle of the current stream of a device (without a Stream object around it)."""
+    return _raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+
+
+def _stream_fast(stream) -> ctypes.c_void_p:
+    if stream is None:
+        return ctypes.c_void_p(raw_stream(torch.cuda.current_device()))
+    return _stream(stream)
+
+
 def dtype_code(dt: torch.dtype) -> int:
     return _DT[dt]
 
@@ -369,7 +383,7 @@ def tq_paged_layout(desc: tq_paged_desc) -> tq_paged:
 
 def tq_paged_init(cache: tq_paged, desc: tq_paged_desc, buf: torch.Tensor, stream=None):
     _check(lib.tq_paged_init(ctypes.byref(cache), ctypes.byref(desc), _ptr(buf),
-                             buf.numel() * buf.element_size(), _stream(stream)), "tq_paged_init")
+                             buf.numel() * buf.element_size(), _stream_fast(stream)), "tq_paged_init")
 
 
 def _tokens(t: torch.Tensor, heads: int, d: int):
@@ -397,7 +411,7 @@ def _rows(slots: torch.Tensor, cu: torch.Tensor) -> int:
 
 def tq_paged_extend(cache: tq_paged, slots, cu, stream=None):
     _check(lib.tq_paged_extend(ctypes.byref(cache), _i32(slots), _i32(cu), _rows(slots, cu),
-                               _stream(stream)), "tq_paged_extend")
+                               _stream_fast(stream)), "tq_paged_extend")
 
 
 def tq_paged_write(cache: tq_paged, layer: int, K, V, stream=None):
@@ -405,17 +419,17 @@ def tq_paged_write(cache: tq_paged, layer: int, K, V, stream=None):
         raise ValueError("K and V have different token counts")
     (kp, ks), (vp, vs) = (_tokens(t, cache.desc.Hkv, cache.desc.d) for t in (K, V))
     _check(lib.tq_paged_write(ctypes.byref(cache), layer, kp, vp, ks, vs, K.shape[0],
-                              _stream(stream)), "tq_paged_write")
+                              _stream_fast(stream)), "tq_paged_write")
 
 
 def tq_paged_read(cache: tq_paged, layer: int, slots, cu, K, V, stream=None):
     _check(lib.tq_paged_read(ctypes.byref(cache), layer, _i32(slots), _i32(cu), _rows(slots, cu),
-                             K.shape[0], _ptr(K), _ptr(V), _stream(stream)), "tq_paged_read")
+                             K.shape[0], _ptr(K), _ptr(V), _stream_fast(stream)), "tq_paged_read")
 
 
 def tq_paged_table(cache: tq_paged, slots, out, stream=None):
     _check(lib.tq_paged_table(ctypes.byref(cache), _i32(slots), slots.numel(), _ptr(out),
-                              _stream(stream)), "tq_paged_table")
+                              _stream_fast(stream)), "tq_paged_table")
 
 
 def tq_paged_workspace_bytes(cache: tq_paged) -> int:
@@ -424,7 +438,7 @@ def tq_paged_workspace_bytes(cache: tq_paged) -> int:
 
 def tq_paged_workspace_init(cache: tq_paged, workspace, stream=None):
     _check(lib.tq_paged_workspace_init(ctypes.byref(cache), _ptr(workspace), _ws(workspace),
-                                       _stream(stream)), "tq_paged_workspace_init")
+                                       _stream_fast(stream)), "tq_paged_workspace_init")
 
 
 def tq_paged_attention(cache: tq_paged, layer: int, Q, slots, cu, max_q: int, causal: bool,
@@ -435,7 +449,7 @@ def tq_paged_attention(cache: tq_paged, layer: int, Q, slots, cu, max_q: int, ca
     _check(lib.tq_paged_attention(ctypes.byref(cache), layer, qp, qs, Hq, _i32(slots), _i32(cu),
                                   _rows(slots, cu), max_q, Q.shape[0], int(causal), softmax_scale,
                                   _ptr(out), _ptr(lse), _ptr(workspace), _ws(workspace),
-                                  _stream(stream)), "tq_paged_attention")
+                                  _stream_fast(stream)), "tq_paged_attention")
 
 
 def _pairs(src, dst) -> int:
@@ -446,28 +460,28 @@ def _pairs(src, dst) -> int:
 
 def tq_paged_fork(cache: tq_paged, src, dst, stream=None):
     _check(lib.tq_paged_fork(ctypes.byref(cache), _i32(src), _i32(dst), _pairs(src, dst),
-                             _stream(stream)), "tq_paged_fork")
+                             _stream_fast(stream)), "tq_paged_fork")
 
 
 def tq_paged_copy(cache: tq_paged, to_cache: tq_paged, src, dst, stream=None):
     _check(lib.tq_paged_copy(ctypes.byref(cache), ctypes.byref(to_cache), _i32(src), _i32(dst),
-                             _pairs(src, dst), _stream(stream)), "tq_paged_copy")
+                             _pairs(src, dst), _stream_fast(stream)), "tq_paged_copy")
 
 
 def tq_paged_free(cache: tq_paged, slots, stream=None):
-    _check(lib.tq_paged_free(ctypes.byref(cache), _i32(slots), slots.numel(), _stream(stream)),
+    _check(lib.tq_paged_free(ctypes.byref(cache), _i32(slots), slots.numel(), _stream_fast(stream)),
            "tq_paged_free")
 
 
 def tq_paged_compact(cache: tq_paged, stream=None):
-    _check(lib.tq_paged_compact(ctypes.byref(cache), _stream(stream)), "tq_paged_compact")
+    _check(lib.tq_paged_compact(ctypes.byref(cache), _stream_fast(stream)), "tq_paged_compact")
 
 
 def tq_paged_check(cache: tq_paged, stream=None) -> int:
     """Raise if a call on the cache failed a device check since the last one (waits for the
     stream; clears the status); returns the number of free pages."""
     free = ctypes.c_int32()
-    _check(lib.tq_paged_check(ctypes.byref(cache), ctypes.byref(free), _stream(stream)),
+    _check(lib.tq_paged_check(ctypes.byref(cache), ctypes.byref(free), _stream_fast(stream)),
            "tq_paged_check")
     return free.value
 
