@@ -129,33 +129,47 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
   Cursor nxt = cur;                         // the unit of the tile to request next
   const DecWs ws = dec_ws(a.ws);
 
-  // ---- requests: tile x belongs to warp x mod 4; the page of the next one is read ahead
-  int64_t xi = x0 + ((warp - x0) & (kDecWarps - 1));
-  int nvis = 0, npid = 0, nsub = 0;
-  auto look = [&]() {                       // the tile at xi: its unit, and this lane's sub-block
-    nvis = 0;
-    if (xi >= x1) return;
-    while (xi >= nxt.u0 + nxt.nt) next_unit<kDecRows, kTile, 0>(g, a, G, nxt);
-    nvis = group_visible<kDecRows>(nxt.s, G, nxt.rg, a.causal);
-    if (nvis > 0 && lane < NSUB) {
-      // sub-blocks past the end repeat the last one: masked, but finite
-      const int t = min((int)(xi - nxt.u0) * kTile + lane * SUB, nxt.s.len - 1);
-      npid = g.table[(int64_t)nxt.s.slot * g.max_pages + t / g.page];
-      nsub = t % g.page / SUB;
+  // ---- requests: tile x belongs to warp x mod 4.  The pages of the warp's next tiles of a unit come 32
+  // at a time: lane k holds that of sub-block k mod NSUB of the (k / NSUB)-th of them.
+  constexpr int kBatch = 32 / NSUB;
+  const int lpage = 31 - __clz(g.page);
+  int64_t xi = x0 + ((warp - x0) & (kDecWarps - 1)), xb = xi;      // the next tile, the batch's first
+  int nvis = 0, pids = 0;
+  auto batch = [&]() {
+    xb = xi;
+    const int64_t t = (xi - nxt.u0 + (int64_t)(lane / NSUB) * kDecWarps) * kTile + (lane % NSUB) * SUB;
+    // sub-blocks past the end repeat the last one: masked, but finite
+    const int tk = (int)min(t, (int64_t)nxt.s.len - 1);
+    pids = g.table[(int64_t)nxt.s.slot * g.max_pages + (tk >> lpage)];
+  };
+  // Find the tile at xi; tiles of a unit that sees nothing have nothing to load.
+  auto look = [&]() {
+    for (; xi < x1; xi += kDecWarps) {
+      if (xi >= nxt.u0 + nxt.nt || nvis == 0) {
+        while (xi >= nxt.u0 + nxt.nt) next_unit<kDecRows, kTile, 0>(g, a, G, nxt);
+        nvis = group_visible<kDecRows>(nxt.s, G, nxt.rg, a.causal);
+        if (nvis == 0) continue;
+        batch();
+      } else if (xi >= xb + kBatch * kDecWarps) {
+        batch();
+      }
+      return;
     }
   };
   int ist = 0;                              // stage of the next request
   auto request = [&](int kv) {
     uint64_t* bar = &s_full[warp][ist];
     if (lane == 0) mbar_expect_tx(bar, kBytes);
-    __syncwarp();
+    int pid = __shfl_sync(0xffffffffu, pids, (int)((xi - xb) / kDecWarps) * NSUB + (lane & (NSUB - 1)));
     if (lane < NSUB) {
-      if ((unsigned)npid >= (unsigned)g.pages) {
+      if ((unsigned)pid >= (unsigned)g.pages) {
         atomicOr(&g.state->status, kPagedBadPage);
-        npid = 0;
+        pid = 0;
       }
-      cache_bulk_load(ring + ist * STB + lane * SS, paged_block(g, a.layer, npid, kv, nxt.h, nsub), SUB * D + kPagedTrailer,
-                      bar, g.base, g.total, 401);
+      const int tk = min((int)(xi - nxt.u0) * kTile + lane * SUB, nxt.s.len - 1);
+      cache_bulk_load(ring + ist * STB + lane * SS,
+                      paged_block(g, a.layer, pid, kv, nxt.h, (tk & (g.page - 1)) / SUB), SUB * D + kPagedTrailer, bar,
+                      g.base, g.total, 401);
     }
     ist = ist + 1 == NST ? 0 : ist + 1;
   };
@@ -167,19 +181,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
     if (half == 0) {
       xi += kDecWarps;
       look();
-      while (xi < x1 && nvis == 0) {        // nothing to load for a unit that sees nothing
-        xi += kDecWarps;
-        look();
-      }
     }
   };
-  look();
-  while (xi < x1 && nvis == 0) {
-    xi += kDecWarps;
-    look();
-  }
-#pragma unroll
-  for (int s = 0; s < NST; ++s) refill();
   int cst = 0;
   uint32_t cph = 0;
   auto wait_stage = [&]() {
@@ -206,7 +209,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
         qn[j][k] = ok ? load_f(a.Q, tok * a.q_stride + (int64_t)(u.h * G + row % G) * D + NQ * lane + k, g.dtype) : 0.f;
     }
   };
-  bring(cur);
+  bring(cur);                               // (their latency passes behind the first requests')
+  look();
+#pragma unroll
+  for (int st = 0; st < NST; ++st) refill();
 
   int64_t x = x0;
   while (x < x1) {
@@ -273,18 +279,24 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
 #pragma unroll
         for (int w = 0; w < 4; ++w) A[w] = s_q[(4 * j + w) * 32 + lane];
         const int jo = D == 64 ? 0 : (j ^ (gi & 1)) * 64;
+        // four columns' products in turn: each waits for its own last one only
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 kw = *reinterpret_cast<const uint4*>(kb + 2 * i * D + jo);
-          uint32_t b0, b1;
-          expand4<CODE>(kw.x, b0, b1);
-          hmma16816(sc[i], A[0].x, A[0].y, A[0].z, A[0].w, b0, b1);
-          expand4<CODE>(kw.y, b0, b1);
-          hmma16816(sc[i], A[1].x, A[1].y, A[1].z, A[1].w, b0, b1);
-          expand4<CODE>(kw.z, b0, b1);
-          hmma16816(sc[i], A[2].x, A[2].y, A[2].z, A[2].w, b0, b1);
-          expand4<CODE>(kw.w, b0, b1);
-          hmma16816(sc[i], A[3].x, A[3].y, A[3].z, A[3].w, b0, b1);
+        for (int i0 = 0; i0 < 8; i0 += 4) {
+          uint4 kw[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) kw[i] = *reinterpret_cast<const uint4*>(kb + 2 * (i0 + i) * D + jo);
+          auto step = [&](auto word, const uint4& q) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t b0, b1;
+              expand4<CODE>(word(kw[i]), b0, b1);
+              hmma16816(sc[i0 + i], q.x, q.y, q.z, q.w, b0, b1);
+            }
+          };
+          step([](const uint4& v) { return v.x; }, A[0]);
+          step([](const uint4& v) { return v.y; }, A[1]);
+          step([](const uint4& v) { return v.z; }, A[2]);
+          step([](const uint4& v) { return v.w; }, A[3]);
         }
       }
       const float f = fr * *reinterpret_cast<const float*>(ring + cst * STB + 16 * c / SUB * SS + SUB * D);
@@ -337,20 +349,31 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
       const float so = st * (1.f / kUp);
       const unsigned char* vb = ring + cst * STB + 16 * c / SUB * SS + 16 * c % SUB + gi * SUB;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint4 vw = *reinterpret_cast<const uint4*>(vb + n * 8 * SUB);
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t b0, b1;
-        expand4<CODE>(vw.x, b0, b1);
-        hmma16816(acc, ph[0], pl[0], ph[1], pl[1], b0, b1);
-        expand4<CODE>(vw.y, b0, b1);
-        hmma16816(acc, ph[2], pl[2], ph[3], pl[3], b0, b1);
-        expand4<CODE>(vw.z, b0, b1);
-        hmma16816(acc, ph[4], pl[4], ph[5], pl[5], b0, b1);
-        expand4<CODE>(vw.w, b0, b1);
-        hmma16816(acc, ph[6], pl[6], ph[7], pl[7], b0, b1);
-        o[n][0] = fmaf(so, acc[0] + acc[2], o[n][0] * alpha);
-        o[n][1] = fmaf(so, acc[1] + acc[3], o[n][1] * alpha);
+      for (int n0 = 0; n0 < NT; n0 += 4) {
+        uint4 vw[4];
+        float acc[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vw[i] = *reinterpret_cast<const uint4*>(vb + (n0 + i) * 8 * SUB);
+          acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        }
+        auto step = [&](auto word, int j) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t b0, b1;
+            expand4<CODE>(word(vw[i]), b0, b1);
+            hmma16816(acc[i], ph[j], pl[j], ph[j + 1], pl[j + 1], b0, b1);
+          }
+        };
+        step([](const uint4& v) { return v.x; }, 0);
+        step([](const uint4& v) { return v.y; }, 2);
+        step([](const uint4& v) { return v.z; }, 4);
+        step([](const uint4& v) { return v.w; }, 6);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[n0 + i][0] = fmaf(so, acc[i][0] + acc[i][2], o[n0 + i][0] * alpha);
+          o[n0 + i][1] = fmaf(so, acc[i][1] + acc[i][3], o[n0 + i][1] * alpha);
+        }
       }
       __syncwarp();
       next_stage();
@@ -420,18 +443,13 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
         for (int i = 0; i < NT; ++i)
           *reinterpret_cast<float2*>(po + 8 * i + 2 * c) = make_float2(o[i][0], o[i][1]);
         if (c == 0) ws.ml[slot * kDecRows + gi] = make_float2(M, L);
-        __threadfence();
       }
     }
     if (!whole) {
       // the CTA that finishes its part of the unit last joins the parts, in their order
       const int c0 = share_owner(W, C, cur.u0), c1 = share_owner(W, C, ue - 1);
       __syncthreads();
-      if (tid == 0) {
-        __threadfence();
-        s_last = atomicInc(reinterpret_cast<unsigned*>(&ws.count[c0]), (unsigned)(c1 - c0)) == (unsigned)(c1 - c0);
-        __threadfence();
-      }
+      if (tid == 0) s_last = last_part(&ws.count[c0], c1 - c0);
       __syncthreads();
       if (s_last) {
         // 16 threads per row, each D / 16 channels

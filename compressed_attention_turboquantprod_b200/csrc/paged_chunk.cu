@@ -643,13 +643,8 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         ws.lse[slot * R + r] = lse2;
         // the CTA that finishes its part of the unit last joins the parts, in their order
         const int c0 = share_owner(W, C, cur.u0 + kUnitCost), c1 = share_owner(W, C, cur.u0 + kUnitCost + cur.nt - 1);
-        __threadfence();
         tc::bar_sync(1 + wg, 128);
-        if ((r & 127) == 0) {
-          __threadfence();
-          sh.last[wg] = atomicInc(reinterpret_cast<unsigned*>(&ws.count[2 * c0 + wg]), (unsigned)(c1 - c0)) == (unsigned)(c1 - c0);
-          __threadfence();
-        }
+        if ((r & 127) == 0) sh.last[wg] = last_part(&ws.count[2 * c0 + wg], c1 - c0);
         tc::bar_sync(1 + wg, 128);
         if (sh.last[wg]) {
           auto slot_of = [&](int p) { return p == c0 ? 2 * p + 1 : 2 * p; };

@@ -259,6 +259,15 @@ __device__ __forceinline__ int64_t share_ctas(int64_t W, int ctas, int least) {
 __device__ __forceinline__ int64_t share_begin(int64_t W, int64_t C, int64_t c) { return W * c / C; }
 __device__ __forceinline__ int share_owner(int64_t W, int64_t C, int64_t x) { return (int)(((x + 1) * C - 1) / W); }
 
+// One thread, after a barrier of the threads that wrote a part of a unit in `others` + 1 parts: whether
+// this was the last to be written.  The release and acquire at device scope carry the other threads'
+// writes with them; the counter wraps to 0 for the next call.
+__device__ __forceinline__ bool last_part(int* count, int others) {
+  uint32_t old;
+  asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(count), "r"((uint32_t)others) : "memory");
+  return old == (uint32_t)others;
+}
+
 // Whether phase `parity` of an mbarrier is complete (the thread may sleep a little for it).
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
