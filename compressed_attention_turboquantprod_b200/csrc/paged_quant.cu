@@ -76,35 +76,64 @@ __device__ __forceinline__ BlockScale block_scale(float a, int code) {
   return b;
 }
 
-// Stored byte of x.  int8: x * inv is within 127 * 2^-22.9 < 2e-5 of 127 x / a; where that
-// is next to a rounding border the exact products 127 x and (2 n + 1) a / 2 (at most 32
-// significant bits each) are compared in fp64, a tie going to the even code.
+// Stored byte of x, in full.  int8: x * inv is within 127 * 2^-22.9 < 2e-5 of 127 x / a; next to a
+// rounding border the exact products 127 x and (2 n + 1) a / 2 (at most 32 significant bits each) are
+// compared in fp64, a tie going to the even code.  An infinity saturates, a NaN is 0.
 template <int CODE>
-__device__ __forceinline__ uint32_t encode(float x, const BlockScale& b) {
+__device__ __noinline__ uint32_t encode_slow(float x, float a, float inv) {
   if constexpr (CODE == TQ_CODE_INT8) {
-    if (!(fabsf(x) <= b.a)) {                        // an infinity saturates, NaN is 0
-      return x != x || b.inv == 0.f ? 128u : x > 0.f ? 255u : 1u;
-    }
-    const float t = x * b.inv;
-    float r = rintf(t);
-    if (fabsf(fabsf(t - r) - 0.5f) < 4e-5f) {
-      const double h = floor((double)t) + 0.5;
-      const double diff = 127.0 * (double)x - h * (double)b.a;
-      const double lo = h - 0.5;
-      const double even = fmod(lo, 2.0) == 0.0 ? lo : lo + 1.0;
-      r = b.inv == 0.f ? 0.f : (float)(diff < 0.0 ? lo : diff > 0.0 ? lo + 1.0 : even);
-    }
-    return (uint32_t)((int)r + 128);
+    if (x != x || inv == 0.f) return 128u;
+    if (!(fabsf(x) <= a)) return x > 0.f ? 255u : 1u;
+    const double h = floor((double)(x * inv)) + 0.5;
+    const double diff = 127.0 * (double)x - h * (double)a;
+    const double lo = h - 0.5, even = fmod(lo, 2.0) == 0.0 ? lo : lo + 1.0;
+    return (uint32_t)((int)(diff < 0.0 ? lo : diff > 0.0 ? lo + 1.0 : even) + 128);
   } else {
-    if (x != x || b.inv == 0.f) return 0u;
-    return (uint32_t)__nv_cvt_float_to_fp8(x * b.inv, __NV_SATFINITE, __NV_E4M3);
+    return 0u;
+  }
+}
+
+// Stored bytes of four entries.  int8: 1.5 * 2^23 added in one rounding leaves the nearest integer in
+// the low bits; the remainder tells whether x is plain (finite and not next to a border).
+template <int CODE>
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], const BlockScale& b) {
+  if constexpr (CODE == TQ_CODE_INT8) {
+    uint32_t u[4];
+    bool plain = true;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float m = fmaf(x[k], b.inv, 12582912.f);
+      const float rest = fmaf(x[k], b.inv, 12582912.f - m);
+      plain = plain && fabsf(rest) < 0.5f - 4e-5f;
+      u[k] = __float_as_uint(m);
+    }
+    // bytes of the integers, + 128 each
+    uint32_t w = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410) ^ 0x80808080u;
+    if (!plain) {
+      w = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float m = fmaf(x[k], b.inv, 12582912.f);
+        const float rest = fmaf(x[k], b.inv, 12582912.f - m);
+        w |= (fabsf(rest) < 0.5f - 4e-5f ? (__float_as_uint(m) + 128u) & 255u : encode_slow<CODE>(x[k], b.a, b.inv)) << (8 * k);
+      }
+    }
+    return w;
+  } else {
+    uint32_t w = 0;
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      const float2 y = make_float2(x[k] == x[k] ? x[k] * b.inv : 0.f, x[k + 1] == x[k + 1] ? x[k + 1] * b.inv : 0.f);
+      w |= (uint32_t)__nv_cvt_float2_to_fp8x2(b.inv == 0.f ? make_float2(0.f, 0.f) : y, __NV_SATFINITE, __NV_E4M3) << (8 * k);
+    }
+    return w;
   }
 }
 
 template <int CODE>
 __device__ __forceinline__ float decode_byte(uint32_t u) {
   if constexpr (CODE == TQ_CODE_INT8) {
-    return (float)((int)u - 128);
+    return __uint_as_float(0x4b000000u | u) - 8388736.f;       // 2^23 + u, less 2^23 + 128
   } else {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)u, __NV_E4M3)));
   }
@@ -214,48 +243,71 @@ __global__ void __launch_bounds__(kWThreads) k_paged_write(PGeom g, int layer, c
     constexpr int C16 = D / 16;
     for (int i = first * C16 + tid; i < n1 * C16; i += kWThreads) {
       const int t = i / C16, c = i % C16;
-      uint32_t w[4];
-      const T* e = S + t * D + c * 16;
+      T e[16];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = encode<CODE>(to_f<T>(e[4 * k]), b) | encode<CODE>(to_f<T>(e[4 * k + 1]), b) << 8 |
-               encode<CODE>(to_f<T>(e[4 * k + 2]), b) << 16 | encode<CODE>(to_f<T>(e[4 * k + 3]), b) << 24;
+      for (int k = 0; k < (int)sizeof(T); ++k) reinterpret_cast<uint4*>(e)[k] = S4[t * CH + c * (int)sizeof(T) + k];
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x[4] = {to_f<T>(e[4 * k]), to_f<T>(e[4 * k + 1]), to_f<T>(e[4 * k + 2]), to_f<T>(e[4 * k + 3])};
+        w[k] = encode4<CODE>(x, b);
+      }
       const int tb = t % g.sub;
       *reinterpret_cast<uint4*>(blk + (int64_t)(t / g.sub) * g.sb + paged_k_off(D, tb, c * 16)) =
           make_uint4(w[0], w[1], w[2], w[3]);
     }
   } else {
-    // lanes take neighbouring channels; 16 tokens of a channel are one 16-byte store
+    // a lane takes 16 tokens of four neighbouring channels: four 16-byte stores
+    struct alignas(4 * sizeof(T)) Four {
+      T e[4];
+    };
     const int g0 = first / 16, g1 = (n1 + 15) / 16;
-    for (int i = tid; i < (g1 - g0) * D; i += kWThreads) {
-      const int j = i % D, t16 = (g0 + i / D) * 16;
+    for (int i = tid; i < (g1 - g0) * (D / 4); i += kWThreads) {
+      const int j = 4 * (i % (D / 4)), t16 = (g0 + i / (D / 4)) * 16;
       uint8_t* to = blk + (int64_t)(t16 / g.sub) * g.sb + (int64_t)j * g.sub + t16 % g.sub;
-      if (t16 >= first && t16 + 16 <= n1) {
-        uint32_t w[4];
+      const bool all = t16 >= first && t16 + 16 <= n1;
+      uint32_t w[4][4];                            // [channel][four tokens]
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          w[k] = 0;
+      for (int k = 0; k < 4; ++k) {
+        Four f[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) w[k] |= encode<CODE>(to_f<T>(S[(t16 + 4 * k + q) * D + j]), b) << (8 * q);
+        for (int q = 0; q < 4; ++q) f[q] = *reinterpret_cast<const Four*>(S + (t16 + 4 * k + q) * D + j);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          // rows that hold no token of this append may hold anything: their bytes are not stored
+          float x[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int t = t16 + 4 * k + q;
+            x[q] = all || (t >= first && t < n1) ? to_f<T>(f[q].e[ch]) : 0.f;
+          }
+          w[ch][k] = encode4<CODE>(x, b);
         }
-        *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (all) {
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch)
+          *reinterpret_cast<uint4*>(to + ch * g.sub) = make_uint4(w[ch][0], w[ch][1], w[ch][2], w[ch][3]);
       } else {
-        for (int t = max(t16, first); t < min(t16 + 16, n1); ++t)
-          to[t - t16] = (uint8_t)encode<CODE>(to_f<T>(S[t * D + j]), b);
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (t16 + k >= first && t16 + k < n1)
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) to[ch * g.sub + k] = (uint8_t)(w[ch][k >> 2] >> (8 * (k & 3)));
       }
     }
   }
 }
 
 // The first cu[i + 1] - cu[i] tokens of slot slots[i] as floats (zeros past its length).
-// One CTA per (up to read_tokens tokens of one sequence, head, K / V).
-template <typename T, int D>
-constexpr int read_tokens() { return D * sizeof(T) >= 1024 ? 32 : 64; }     // static shared memory
+// One CTA per (up to 64 tokens of one sequence, head, K / V); no shared memory: a lane's 16 key codes
+// are neighbours in the output already, and of values it takes 16 tokens of four neighbouring channels and
+// turns them around in 4 x 4 bytes.
+constexpr int kReadTokens = 64;
 template <typename T, int D, int CODE>
 __global__ void __launch_bounds__(kWThreads) k_paged_read(PGeom g, int layer, const int* slots, const int* cu, int n,
                                                           int64_t total, T* K, T* V) {
-  constexpr int RT = read_tokens<T, D>();
-  __shared__ __align__(16) T s_t[RT * (D + 8)];
+  constexpr int RT = kReadTokens;
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31;
   const int h = blockIdx.y, kv = blockIdx.z;
@@ -288,38 +340,64 @@ __global__ void __launch_bounds__(kWThreads) k_paged_read(PGeom g, int layer, co
     if (tid == 0) atomicOr(&g.state->status, kPagedBadOffsets);
     return;
   }
-  // groups of 16 tokens lie in one sub-block; thread = (group, 16-byte piece)
-  for (int k = tid; k < RT / 16 * D; k += kWThreads) {
-    const int grp = k / D, x = k % D;
-    const int t = t0 + 16 * grp;
-    if (16 * grp >= nt) continue;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    float scale = 0.f;
-    const int pid = t < len ? g.table[(int64_t)slot * g.max_pages + t / g.page] : -1;
-    const int tb = t % g.page % g.sub;
-    if ((unsigned)pid < (unsigned)g.pages) {
-      const uint8_t* blk = paged_block(g, layer, pid, kv, h, t % g.page / g.sub);
-      scale = *reinterpret_cast<const float*>(blk + (int64_t)g.sub * D);
-      // keys: token tb + x / (D / 16), channels 16 (x mod D / 16)...; values: channel x, 16 tokens
-      const int64_t off = kv ? (int64_t)x * g.sub + tb : paged_k_off(D, tb + x / (D / 16), 16 * (x % (D / 16)));
-      raw = *reinterpret_cast<const uint4*>(blk + off);
-    }
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  // four codes to four outputs
+  struct alignas(4 * sizeof(T)) Four {
+    T e[4];
+  };
+  auto four = [&](uint32_t w, float scale) {
+    Four f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int tok = kv ? 16 * grp + e : 16 * grp + x / (D / 16);
-      const int ch = kv ? x : 16 * (x % (D / 16)) + e;
-      const float v = decode_byte<CODE>((w[e >> 2] >> (8 * (e & 3))) & 255u) * scale;
-      s_t[tok * (D + 8) + ch] = from_f<T>(t0 + tok < len ? v : 0.f);
+    for (int k = 0; k < 4; ++k) f.e[k] = from_f<T>(decode_byte<CODE>((w >> (8 * k)) & 255u) * scale);
+    return f;
+  };
+  auto page_of = [&](int t) {                        // -1: no such token
+    return t < len ? g.table[(int64_t)slot * g.max_pages + t / g.page] : -1;
+  };
+  auto row = [&](int t) { return out + (((int64_t)c0 + t0 + t) * g.Hkv + h) * D; };
+  if (kv == 0) {
+    constexpr int C16 = D / 16;
+    for (int k = tid; k < nt * C16; k += kWThreads) {
+      const int t = k / C16, c = k % C16, pid = page_of(t0 + t);
+      uint4 raw = make_uint4(0, 0, 0, 0);
+      float scale = 0.f;
+      if ((unsigned)pid < (unsigned)g.pages) {
+        const int tp = (t0 + t) % g.page;
+        const uint8_t* blk = paged_block(g, layer, pid, 0, h, tp / g.sub);
+        scale = *reinterpret_cast<const float*>(blk + g.sub * D);
+        raw = *reinterpret_cast<const uint4*>(blk + paged_k_off(D, tp % g.sub, 16 * c));
+      }
+      Four* to = reinterpret_cast<Four*>(row(t) + 16 * c);
+      to[0] = four(raw.x, scale);
+      to[1] = four(raw.y, scale);
+      to[2] = four(raw.z, scale);
+      to[3] = four(raw.w, scale);
     }
-  }
-  __syncthreads();
-  constexpr int CH = D * (int)sizeof(T) / 16;
-  constexpr int EP = 16 / (int)sizeof(T);
-  for (int k = tid; k < nt * CH; k += kWThreads) {
-    const int t = k / CH, c = k % CH;
-    *reinterpret_cast<uint4*>(out + (((int64_t)c0 + t0 + t) * g.Hkv + h) * D + c * EP) =
-        *reinterpret_cast<const uint4*>(&s_t[t * (D + 8) + c * EP]);
+  } else {
+    for (int k = tid; k < (nt + 15) / 16 * (D / 4); k += kWThreads) {
+      const int j = 4 * (k % (D / 4)), t = 16 * (k / (D / 4)), pid = page_of(t0 + t);
+      uint4 raw[4] = {};
+      float scale = 0.f;
+      if ((unsigned)pid < (unsigned)g.pages) {
+        const int tp = (t0 + t) % g.page;
+        const uint8_t* blk = paged_block(g, layer, pid, 1, h, tp / g.sub);
+        scale = *reinterpret_cast<const float*>(blk + g.sub * D);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) raw[ch] = *reinterpret_cast<const uint4*>(blk + (j + ch) * g.sub + tp % g.sub);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t a0 = reinterpret_cast<const uint32_t*>(&raw[0])[q], a1 = reinterpret_cast<const uint32_t*>(&raw[1])[q],
+                       a2 = reinterpret_cast<const uint32_t*>(&raw[2])[q], a3 = reinterpret_cast<const uint32_t*>(&raw[3])[q];
+        const uint32_t l01 = __byte_perm(a0, a1, 0x5140), l23 = __byte_perm(a2, a3, 0x5140),
+                       h01 = __byte_perm(a0, a1, 0x7362), h23 = __byte_perm(a2, a3, 0x7362);
+        const uint32_t w[4] = {__byte_perm(l01, l23, 0x5410), __byte_perm(l01, l23, 0x7632),
+                               __byte_perm(h01, h23, 0x5410), __byte_perm(h01, h23, 0x7632)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (t + 4 * q + e < nt)
+            *reinterpret_cast<Four*>(row(t + 4 * q + e) + j) = four(w[e], t0 + t + 4 * q + e < len ? scale : 0.f);
+      }
+    }
   }
 }
 
@@ -338,7 +416,7 @@ cudaError_t write_t(const PGeom& g, int layer, const void* K, const void* V, int
 template <typename T, int D, int CODE>
 cudaError_t read_t(const PGeom& g, int layer, const int* slots, const int* cu, int n, int64_t total, void* K, void* V,
                    cudaStream_t s) {
-  const int64_t items = total / read_tokens<T, D>() + n;
+  const int64_t items = total / kReadTokens + n;
   return launch_pdl(k_paged_read<T, D, CODE>, dim3((unsigned)items, g.Hkv, 2), dim3(kWThreads), 0, s, g, layer, slots,
                     cu, n, total, static_cast<T*>(K), static_cast<T*>(V));
 }
