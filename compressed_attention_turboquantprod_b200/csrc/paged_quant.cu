@@ -11,6 +11,8 @@
 // written; when it does, the page's codes are formed again from the tail.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace tq {
@@ -195,21 +197,34 @@ __global__ void __launch_bounds__(kWThreads) k_paged_write(PGeom g, int layer, c
   const int end = row.start + row.count, p_open = end / g.page;
   const bool old_first = row.start % g.page != 0 && p_open != row.start / g.page;
   const bool keep = p == p_open && !old_first;
-  auto amax4 = [](uint4 v) {
-    const T* e = reinterpret_cast<const T*>(&v);
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < EP; ++i) m = fmaxf(m, finite_abs(to_f<T>(e[i])));
-    return m;
+  // The largest magnitude, as bits: entries without their sign compare as integers; one that is not
+  // finite shows itself past the largest finite number, and only then are they sorted out.
+  constexpr uint32_t kFinite = std::is_same_v<T, float> ? 0x7f7fffffu : std::is_same_v<T, __half> ? 0x7bffu : 0x7f7fu;
+  auto bits = [&](uint32_t m, uint32_t u) {
+    if constexpr (sizeof(T) == 4) return max(m, u & 0x7fffffffu);
+    else return __vmaxu2(m, u & 0x7fff7fffu);
   };
-  float a = 0.f;
+  uint32_t m = 0;
 #pragma unroll 4
   for (int i = tid; i < (n1 - n0) * CH; i += kWThreads) {
     const int t = i / CH, c = i % CH;
     const uint4 v = *reinterpret_cast<const uint4*>(in + (src0 + t) * stride + (int64_t)h * D + c * EP);
     S4[(n0 + t) * CH + c] = v;
     if (keep) tail[(n0 + t) * CH + c] = v;
-    a = fmaxf(a, amax4(v));
+    m = bits(bits(bits(bits(m, v.x), v.y), v.z), v.w);
+  }
+  if constexpr (sizeof(T) == 2) m = max(m & 0xffffu, m >> 16);
+  float a = 0.f;
+  if (m <= kFinite) {
+    if constexpr (sizeof(T) == 4) {
+      a = __uint_as_float(m);
+    } else {
+      const uint16_t m16 = (uint16_t)m;
+      a = to_f<T>(*reinterpret_cast<const T*>(&m16));
+    }
+  } else {
+    for (int i = tid; i < (n1 - n0) * CH; i += kWThreads)
+      for (int k = 0; k < EP; ++k) a = fmaxf(a, finite_abs(to_f<T>(S[(n0 * CH + i) * EP + k])));
   }
   a = cta_max(a, s_red);
   int first = n0;
@@ -265,35 +280,31 @@ __global__ void __launch_bounds__(kWThreads) k_paged_write(PGeom g, int layer, c
     for (int i = tid; i < (g1 - g0) * (D / 4); i += kWThreads) {
       const int j = 4 * (i % (D / 4)), t16 = (g0 + i / (D / 4)) * 16;
       uint8_t* to = blk + (int64_t)(t16 / g.sub) * g.sb + (int64_t)j * g.sub + t16 % g.sub;
-      const bool all = t16 >= first && t16 + 16 <= n1;
-      uint32_t w[4][4];                            // [channel][four tokens]
+      if (t16 >= first && t16 + 16 <= n1) {
+        uint32_t w[4][4];                          // [channel][four tokens]
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        Four f[4];
+        for (int k = 0; k < 4; ++k) {
+          Four f[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) f[q] = *reinterpret_cast<const Four*>(S + (t16 + 4 * k + q) * D + j);
+          for (int q = 0; q < 4; ++q) f[q] = *reinterpret_cast<const Four*>(S + (t16 + 4 * k + q) * D + j);
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          // rows that hold no token of this append may hold anything: their bytes are not stored
-          float x[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int t = t16 + 4 * k + q;
-            x[q] = all || (t >= first && t < n1) ? to_f<T>(f[q].e[ch]) : 0.f;
+          for (int ch = 0; ch < 4; ++ch) {
+            const float x[4] = {to_f<T>(f[0].e[ch]), to_f<T>(f[1].e[ch]), to_f<T>(f[2].e[ch]), to_f<T>(f[3].e[ch])};
+            w[ch][k] = encode4<CODE>(x, b);
           }
-          w[ch][k] = encode4<CODE>(x, b);
         }
-      }
-      if (all) {
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch)
           *reinterpret_cast<uint4*>(to + ch * g.sub) = make_uint4(w[ch][0], w[ch][1], w[ch][2], w[ch][3]);
       } else {
+        // a group that this append fills in part: byte by byte
+        for (int t = max(t16, first); t < min(t16 + 16, n1); ++t) {
+          const Four f = *reinterpret_cast<const Four*>(S + t * D + j);
+          const float x[4] = {to_f<T>(f.e[0]), to_f<T>(f.e[1]), to_f<T>(f.e[2]), to_f<T>(f.e[3])};
+          const uint32_t w = encode4<CODE>(x, b);
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (t16 + k >= first && t16 + k < n1)
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) to[ch * g.sub + k] = (uint8_t)(w[ch][k >> 2] >> (8 * (k & 3)));
+          for (int ch = 0; ch < 4; ++ch) to[ch * g.sub + t - t16] = (uint8_t)(w >> (8 * ch));
+        }
       }
     }
   }
