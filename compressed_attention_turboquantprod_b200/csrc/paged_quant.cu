@@ -78,8 +78,8 @@ __device__ __forceinline__ BlockScale block_scale(float a, int code) {
   return b;
 }
 
-// Stored byte of x, in full.  int8: x * inv is within 127 * 2^-22.9 < 2e-5 of 127 x / a; next to a
-// rounding border the exact products 127 x and (2 n + 1) a / 2 (at most 32 significant bits each) are
+// Stored byte of x, in full.  int8: inv is off by 2^-24 at most, so x * inv is within 127 * 2^-24 <
+// 8e-6 of 127 x / a; next to a rounding border the exact products 127 x and (2 n + 1) a / 2 (at most 32 significant bits each) are
 // compared in fp64, a tie going to the even code.  An infinity saturates, a NaN is 0.
 template <int CODE>
 __device__ __noinline__ uint32_t encode_slow(float x, float a, float inv) {
@@ -88,7 +88,7 @@ __device__ __noinline__ uint32_t encode_slow(float x, float a, float inv) {
     if (!(fabsf(x) <= a)) return x > 0.f ? 255u : 1u;
     const double h = floor((double)(x * inv)) + 0.5;
     const double diff = 127.0 * (double)x - h * (double)a;
-    const double lo = h - 0.5, even = fmod(lo, 2.0) == 0.0 ? lo : lo + 1.0;
+    const double lo = h - 0.5, even = ((int)lo & 1) == 0 ? lo : lo + 1.0;
     return (uint32_t)((int)(diff < 0.0 ? lo : diff > 0.0 ? lo + 1.0 : even) + 128);
   } else {
     return 0u;
@@ -106,7 +106,7 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], const BlockScal
     for (int k = 0; k < 4; ++k) {
       const float m = fmaf(x[k], b.inv, 12582912.f);
       const float rest = fmaf(x[k], b.inv, 12582912.f - m);
-      plain = plain && fabsf(rest) < 0.5f - 4e-5f;
+      plain = plain && fabsf(rest) < 0.5f - 1e-5f;
       u[k] = __float_as_uint(m);
     }
     // bytes of the integers, + 128 each
@@ -117,7 +117,7 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[4], const BlockScal
       for (int k = 0; k < 4; ++k) {
         const float m = fmaf(x[k], b.inv, 12582912.f);
         const float rest = fmaf(x[k], b.inv, 12582912.f - m);
-        w |= (fabsf(rest) < 0.5f - 4e-5f ? (__float_as_uint(m) + 128u) & 255u : encode_slow<CODE>(x[k], b.a, b.inv)) << (8 * k);
+        w |= (fabsf(rest) < 0.5f - 1e-5f ? (__float_as_uint(m) + 128u) & 255u : encode_slow<CODE>(x[k], b.a, b.inv)) << (8 * k);
       }
     }
     return w;
@@ -157,20 +157,32 @@ __device__ __forceinline__ float cta_max(float v, float* s) {
 // are encoded; codes leave as 16-byte words.
 template <typename T, int D, int CODE>
 __global__ void __launch_bounds__(kWThreads) k_paged_write(PGeom g, int layer, const T* K, const T* V, int64_t k_stride,
-                                                           int64_t v_stride, int64_t total) {
+                                                           int64_t v_stride, int64_t total, int max_rows) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float s_red[kWThreads / 32];
   pdl_wait();
   const int tid = threadIdx.x;
   const int item = blockIdx.x, h = blockIdx.y, kv = blockIdx.z;
-  const PagedState* st = g.state;
-  if (item >= st->n_items) return;
-  int lo = 0, hi = st->n_rows;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (g.rows[mid].item <= item) lo = mid; else hi = mid;
+  // the row whose items hold this one: up to 32 rows by one load each, more by bisection
+  const int n_items = g.state->n_items, n_rows = g.state->n_rows, lane = tid & 31;
+  PagedRow row = g.rows[lane < max_rows ? lane : 0];
+  if (item >= n_items) return;
+  if (n_rows <= 32) {
+    const unsigned below = __ballot_sync(0xffffffffu, lane < n_rows && row.item <= item);
+    const int l = 31 - __clz(below);
+    row.slot = __shfl_sync(0xffffffffu, row.slot, l);
+    row.src = __shfl_sync(0xffffffffu, row.src, l);
+    row.start = __shfl_sync(0xffffffffu, row.start, l);
+    row.count = __shfl_sync(0xffffffffu, row.count, l);
+    row.item = __shfl_sync(0xffffffffu, row.item, l);
+  } else {
+    int lo = 0, hi = n_rows;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (g.rows[mid].item <= item) lo = mid; else hi = mid;
+    }
+    row = g.rows[lo];
   }
-  const PagedRow row = g.rows[lo];
   const int p = row.start / g.page + (item - row.item);
   const int t0 = p * g.page;
   const int n0 = max(row.start, t0) - t0, n1 = min(row.start + row.count, t0 + g.page) - t0;
@@ -421,7 +433,7 @@ cudaError_t write_t(const PGeom& g, int layer, const void* K, const void* V, int
   // a row of c tokens touches at most c / page + 2 pages
   const int64_t items = total / g.page + 2 * (int64_t)n_rows;
   return launch_pdl(k_paged_write<T, D, CODE>, dim3((unsigned)items, g.Hkv, 2), dim3(kWThreads), smem, s, g, layer,
-                    static_cast<const T*>(K), static_cast<const T*>(V), ks, vs, total);
+                    static_cast<const T*>(K), static_cast<const T*>(V), ks, vs, total, n_rows);
 }
 
 template <typename T, int D, int CODE>
