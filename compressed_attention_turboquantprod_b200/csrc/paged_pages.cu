@@ -16,23 +16,24 @@ constexpr int kPlanThreads = 1024;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveChunk = 16384;      // bytes a CTA moves per item
 
-// Inclusive prefix sum over the CTA (kPlanThreads threads), `s` of 33 ints; every thread
+// Inclusive prefix sum over the CTA (kPlanThreads threads), `s` of 32 entries; every thread
 // gets its own sum, *all the total.
-__device__ __forceinline__ int block_scan(int v, int* s, int* all) {
+template <typename I>
+__device__ __forceinline__ I block_scan(I v, I* s, I* all) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    const I u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   __syncthreads();                     // s may still be read from the last call
   if (lane == 31) s[w] = v;
   __syncthreads();
   if (w == 0) {
-    int t = s[lane];
+    I t = s[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, t, o);
+      const I u = __shfl_up_sync(0xffffffffu, t, o);
       if (lane >= o) t += u;
     }
     s[lane] = t;
@@ -92,6 +93,7 @@ __device__ __forceinline__ int find_row(const int* scan, int n, int x) {
 
 __global__ void k_paged_init(PGeom g) {
   pdl_wait();
+  pdl_launch_dependents();
   for (int i = threadIdx.x; i < g.slots; i += kPlanThreads) g.claim[i] = -1;
   if (threadIdx.x == 0) g.state->n_free = g.pages;
 }
@@ -101,8 +103,10 @@ __global__ void k_paged_init(PGeom g) {
 // out).  All or nothing: any error sets a status bit and the plan stays empty.
 __global__ void __launch_bounds__(kPlanThreads, 1) k_paged_extend(PGeom g, const int* slots, const int* cu, int n) {
   __shared__ int s_scan[32];
+  __shared__ unsigned long long s_scan2[32];
   __shared__ int s_bad, s_need, s_items;
   pdl_wait();
+  pdl_launch_dependents();
   const int tid = threadIdx.x;
   if (tid == 0) {
     s_bad = 0;
@@ -141,8 +145,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) k_paged_extend(PGeom g, const
       g.rows[i] = PagedRow{slot, a, start, count, 0};
     }
     if (bad) atomicOr(&s_bad, bad);
-    int all_n, all_i;
-    const int rn = block_scan(need, s_scan, &all_n), ri = block_scan(items, s_scan, &all_i);
+    unsigned long long all;                      // both sums in one scan
+    const unsigned long long r = block_scan((unsigned long long)need << 32 | (unsigned)items, s_scan2, &all);
+    const int rn = (int)(r >> 32), ri = (int)(r & 0xffffffffu), all_n = (int)(all >> 32), all_i = (int)(all & 0xffffffffu);
     if (i < n) {
       g.scan[i] = s_need + rn - need;
       g.rows[i].item = s_items + ri - items;
@@ -186,6 +191,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) k_paged_extend(PGeom g, const
 __global__ void __launch_bounds__(kMoveThreads) k_paged_free(PGeom g, const int* slots, int n) {
   __shared__ int s_len;
   pdl_wait();
+  pdl_launch_dependents();
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int slot = slots[i];
     __syncthreads();
@@ -225,6 +231,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) k_paged_branch(PGeom src, PGe
   __shared__ int s_scan[32];
   __shared__ int s_bad, s_need;
   pdl_wait();
+  pdl_launch_dependents();
   const int tid = threadIdx.x;
   const bool same = src.base == dst.base;
   if (tid == 0) {
@@ -297,6 +304,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) k_paged_branch(PGeom src, PGe
 __global__ void __launch_bounds__(kPlanThreads, 1) k_paged_compact(PGeom g) {
   __shared__ int s_scan[32];
   pdl_wait();
+  pdl_launch_dependents();
   const int tid = threadIdx.x;
   const int live = g.pages - g.state->n_free;
   int holes = 0, high = 0;
@@ -352,6 +360,7 @@ __device__ __forceinline__ void copy16(uint8_t* to, const uint8_t* from, int64_t
 __global__ void __launch_bounds__(kMoveThreads) k_paged_move(PGeom src, PGeom dst, const int* from, const int* to,
                                                              int share) {
   pdl_wait();
+  pdl_launch_dependents();
   const PagedState st = *dst.state;
   const int nch = (int)((dst.page_bytes + kMoveChunk - 1) / kMoveChunk);
   const int64_t items = (int64_t)st.n_moves * dst.layers * nch;
@@ -401,6 +410,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_paged_move(PGeom src, PGeom ds
 // Rows of the page table, -1 where a sequence has no page.
 __global__ void __launch_bounds__(kMoveThreads) k_paged_table(PGeom g, const int* slots, int n, int* out) {
   pdl_wait();
+  pdl_launch_dependents();
   for (int64_t i = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x; i < (int64_t)n * g.max_pages;
        i += (int64_t)gridDim.x * kMoveThreads) {
     const int slot = slots[i / g.max_pages], p = (int)(i % g.max_pages);

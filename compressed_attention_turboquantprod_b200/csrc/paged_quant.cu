@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(kWThreads) k_paged_write(PGeom g, int layer, c
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float s_red[kWThreads / 32];
   pdl_wait();
+  pdl_launch_dependents();
   const int tid = threadIdx.x;
   const int item = blockIdx.x, h = blockIdx.y, kv = blockIdx.z;
   // the row whose items hold this one: up to 32 rows by one load each, more by bisection
@@ -332,6 +333,7 @@ __global__ void __launch_bounds__(kWThreads) k_paged_read(PGeom g, int layer, co
                                                           int64_t total, T* K, T* V) {
   constexpr int RT = kReadTokens;
   pdl_wait();
+  pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
   const int h = blockIdx.y, kv = blockIdx.z;
   // the sequence and tile of this CTA: rows in groups of 32, one per lane
