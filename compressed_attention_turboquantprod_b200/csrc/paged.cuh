@@ -129,6 +129,7 @@ struct PagedAttn {
   int causal;
   float scale;
   void* ws;
+  size_t ws_bytes;
 };
 size_t paged_attn_ws_bytes(int d);
 // many query rows (paged_chunk.cu)

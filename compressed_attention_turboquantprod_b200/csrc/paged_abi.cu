@@ -43,8 +43,8 @@ int layout_status(const tq_paged_desc* d, tq_paged* out) {
     return set_error(TQ_ERR_UNSUPPORTED, "page=%d not in {16,32,64,128}", d->page);
   if (d->code != TQ_CODE_INT8 && d->code != TQ_CODE_E4M3)
     return set_error(TQ_ERR_UNSUPPORTED, "code=%d is neither int8 nor e4m3", d->code);
-  if ((int64_t)d->max_pages * d->page > INT_MAX)
-    return set_error(TQ_ERR_UNSUPPORTED, "max_pages * page = %lld tokens do not fit in 31 bits",
+  if ((int64_t)d->max_pages * d->page > (1 << 30))
+    return set_error(TQ_ERR_UNSUPPORTED, "max_pages * page = %lld tokens, more than 2^30",
                      (long long)d->max_pages * d->page);
   tq_paged c;
   std::memset(&c, 0, sizeof(c));
@@ -266,6 +266,11 @@ int tq_paged_attention(const tq_paged* c, int layer, const void* Q, int64_t q_st
   if (bad_stride(c, q_stride, Hq))
     return set_error(TQ_ERR_INVALID_ARG, "tq_paged_attention: q_stride=%lld: at least Hq * d, a multiple of 16 bytes",
                      (long long)q_stride);
+  // several CTAs read a query that one of them answers: the output may not lie over the queries
+  const int64_t es = tq::paged_esize(c->desc.dtype), row = (int64_t)Hq * c->desc.d * es;
+  const char *qb = static_cast<const char*>(Q), *ob = static_cast<const char*>(out);
+  if (ob < qb + (total_q - 1) * q_stride * es + row && qb < ob + total_q * row)
+    return set_error(TQ_ERR_INVALID_ARG, "tq_paged_attention: out overlaps Q");
   if (!workspace || !aligned(workspace, 256) || ws_bytes < tq::paged_attn_ws_bytes(c->desc.d))
     return set_error(TQ_ERR_INVALID_ARG, "tq_paged_attention: workspace must be 256-byte aligned, %zu bytes",
                      tq::paged_attn_ws_bytes(c->desc.d));
@@ -286,6 +291,7 @@ int tq_paged_attention(const tq_paged* c, int layer, const void* Q, int64_t q_st
   a.causal = causal != 0;
   a.scale = softmax_scale;
   a.ws = workspace;
+  a.ws_bytes = ws_bytes;
   return done(tq::paged_launch_attention(geom(c), a, static_cast<cudaStream_t>(stream)), "tq_paged_attention");
 }
 

@@ -426,7 +426,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
         o[i][1] += v.y;
       }
       if (whole) {
-        if (gi < rows && otok >= 0 && otok < a.total_q) {
+        if (gi < rows && otok >= 0 && otok < a.total_q &&
+            TQ_CHECKED(static_cast<char*>(a.out) + (otok * a.Hq + ohq) * D * paged_esize(g.dtype), D * paged_esize(g.dtype), a.out,
+                       a.total_q * a.Hq * D * paged_esize(g.dtype), 402)) {
           const float inv = L > 0.f ? 1.f / L : 0.f;
           const int64_t at = (otok * a.Hq + ohq) * D;
 #pragma unroll
@@ -439,6 +441,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
       } else {
         const int slot = 2 * cta + (x == cur.u0 ? 1 : 0);
         float* po = ws.o + ((int64_t)slot * kDecRows + gi) * D;
+        if (TQ_CHECKED(po, 4 * D, a.ws, (int64_t)a.ws_bytes, 403))
 #pragma unroll
         for (int i = 0; i < NT; ++i)
           *reinterpret_cast<float2*>(po + 8 * i + 2 * c) = make_float2(o[i][0], o[i][1]);

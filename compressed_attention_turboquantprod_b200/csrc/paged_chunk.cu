@@ -607,7 +607,8 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
           const int rr = 32 * w4 + i * RI + lane / RL, c = lane % RL;
           const int64_t at = place(128 * wg + rr, (int64_t)a.Hq * D);
           const uint4 v = nt > 0 ? *reinterpret_cast<const uint4*>(Q + sw_off<128>(rr, c)) : make_uint4(0, 0, 0, 0);
-          if (at >= 0) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at)[c] = v;
+          if (at >= 0 && TQ_CHECKED(static_cast<uint16_t*>(a.out) + at, 2 * D, a.out, a.total_q * a.Hq * D * 2, 423))
+            reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at)[c] = v;
         }
         __syncwarp();
       };
@@ -625,7 +626,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
           if (whole) {
             *reinterpret_cast<uint4*>(Q + sw_off<128>(r & 127, 4 * c + i)) =
                 make_uint4(pack2(o[0], o[1], f16), pack2(o[2], o[3], f16), pack2(o[4], o[5], f16), pack2(o[6], o[7], f16));
-          } else {
+          } else if (TQ_CHECKED(&part[(int64_t)(8 * c + 2 * i + 1) * R], 16, a.ws, (int64_t)a.ws_bytes, 424)) {
             part[(int64_t)(8 * c + 2 * i) * R] = make_float4(o[0], o[1], o[2], o[3]);
             part[(int64_t)(8 * c + 2 * i + 1) * R] = make_float4(o[4], o[5], o[6], o[7]);
           }

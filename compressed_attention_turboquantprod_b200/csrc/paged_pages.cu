@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) k_paged_extend(PGeom g, const
     take_pages(g, need, s_scan, [&](int r, int page) {
       const int i = find_row(g.scan, n, r);
       const PagedRow w = g.rows[i];
-      g.table[(int64_t)w.slot * g.max_pages + (w.start + g.page - 1) / g.page + (r - g.scan[i])] = page;
+      int* to = &g.table[(int64_t)w.slot * g.max_pages + (w.start + g.page - 1) / g.page + (r - g.scan[i])];
+      if (TQ_CHECKED(to, 4, g.table, 4 * (int64_t)g.slots * g.max_pages, 445)) *to = page;
     });
   for (int i = tid; i < n; i += kPlanThreads) {
     const PagedRow w = g.rows[i];
@@ -374,6 +375,9 @@ __global__ void __launch_bounds__(kMoveThreads) k_paged_move(PGeom src, PGeom ds
       continue;
     }
     const int64_t o = (int64_t)ch * kMoveChunk;
+    if (!TQ_CHECKED(dst.pool + ((int64_t)layer * dst.pages + m.y) * dst.page_bytes, dst.page_bytes, dst.base, dst.total, 441) ||
+        !TQ_CHECKED(src.pool + ((int64_t)layer * src.pages + m.x) * src.page_bytes, src.page_bytes, src.base, src.total, 442))
+      continue;
     copy16(dst.pool + ((int64_t)layer * dst.pages + m.y) * dst.page_bytes + o,
            src.pool + ((int64_t)layer * src.pages + m.x) * src.page_bytes + o,
            min((int64_t)kMoveChunk, dst.page_bytes - o));
@@ -395,6 +399,9 @@ __global__ void __launch_bounds__(kMoveThreads) k_paged_move(PGeom src, PGeom ds
     const int a = from[i], b = to[i], len = dst.len[b];
     if (k < per) {
       const int layer = k / (2 * dst.Hkv), kvh = k % (2 * dst.Hkv);
+      if (!TQ_CHECKED(paged_tail(dst, layer, b, 0, kvh), dst.tail_head, dst.base, dst.total, 443) ||
+          !TQ_CHECKED(paged_tail(src, layer, a, 0, kvh), src.tail_head, src.base, src.total, 444))
+        continue;
       copy16(paged_tail(dst, layer, b, 0, kvh), paged_tail(src, layer, a, 0, kvh),
              (int64_t)(len % dst.page) * dst.d * es);
     } else if (share) {

@@ -221,9 +221,12 @@ __global__ void __launch_bounds__(kWThreads) k_paged_write(PGeom g, int layer, c
 #pragma unroll 4
   for (int i = tid; i < (n1 - n0) * CH; i += kWThreads) {
     const int t = i / CH, c = i % CH;
-    const uint4 v = *reinterpret_cast<const uint4*>(in + (src0 + t) * stride + (int64_t)h * D + c * EP);
+    const T* from = in + (src0 + t) * stride + (int64_t)h * D + c * EP;
+    const uint4 v = TQ_CHECKED(from, 16, in, ((total - 1) * stride + (int64_t)g.Hkv * D) * (int64_t)sizeof(T), 431)
+                        ? *reinterpret_cast<const uint4*>(from)
+                        : make_uint4(0, 0, 0, 0);
     S4[(n0 + t) * CH + c] = v;
-    if (keep) tail[(n0 + t) * CH + c] = v;
+    if (keep && TQ_CHECKED(&tail[(n0 + t) * CH + c], 16, g.base, g.total, 432)) tail[(n0 + t) * CH + c] = v;
     m = bits(bits(bits(bits(m, v.x), v.y), v.z), v.w);
   }
   if constexpr (sizeof(T) == 2) m = max(m & 0xffffu, m >> 16);
@@ -281,8 +284,8 @@ __global__ void __launch_bounds__(kWThreads) k_paged_write(PGeom g, int layer, c
         w[k] = encode4<CODE>(x, b);
       }
       const int tb = t % g.sub;
-      *reinterpret_cast<uint4*>(blk + (int64_t)(t / g.sub) * g.sb + paged_k_off(D, tb, c * 16)) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+      uint8_t* to = blk + (int64_t)(t / g.sub) * g.sb + paged_k_off(D, tb, c * 16);
+      if (TQ_CHECKED(to, 16, g.base, g.total, 433)) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   } else {
     // a lane takes 16 tokens of four neighbouring channels: four 16-byte stores
@@ -293,6 +296,7 @@ __global__ void __launch_bounds__(kWThreads) k_paged_write(PGeom g, int layer, c
     for (int i = tid; i < (g1 - g0) * (D / 4); i += kWThreads) {
       const int j = 4 * (i % (D / 4)), t16 = (g0 + i / (D / 4)) * 16;
       uint8_t* to = blk + (int64_t)(t16 / g.sub) * g.sb + (int64_t)j * g.sub + t16 % g.sub;
+      if (!TQ_CHECKED(to, 3 * g.sub + 16, g.base, g.total, 434)) continue;
       if (t16 >= first && t16 + 16 <= n1) {
         uint32_t w[4][4];                          // [channel][four tokens]
 #pragma unroll
@@ -389,9 +393,11 @@ __global__ void __launch_bounds__(kWThreads) k_paged_read(PGeom g, int layer, co
         const int tp = (t0 + t) % g.page;
         const uint8_t* blk = paged_block(g, layer, pid, 0, h, tp / g.sub);
         scale = *reinterpret_cast<const float*>(blk + g.sub * D);
-        raw = *reinterpret_cast<const uint4*>(blk + paged_k_off(D, tp % g.sub, 16 * c));
+        if (TQ_CHECKED(blk, g.sb, g.base, g.total, 435))
+          raw = *reinterpret_cast<const uint4*>(blk + paged_k_off(D, tp % g.sub, 16 * c));
       }
       Four* to = reinterpret_cast<Four*>(row(t) + 16 * c);
+      if (!TQ_CHECKED(to, 4 * sizeof(Four), out, total * g.Hkv * D * (int64_t)sizeof(T), 436)) continue;
       to[0] = four(raw.x, scale);
       to[1] = four(raw.y, scale);
       to[2] = four(raw.z, scale);

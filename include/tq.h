@@ -519,7 +519,7 @@ typedef struct tq_paged_desc {
   int32_t page;       /* tokens per page: 16, 32, 64 or 128                  */
   int32_t pages;      /* pages in the pool, 1..2^20                          */
   int32_t slots;      /* sequences, 1..65536                                 */
-  int32_t max_pages;  /* pages a sequence may have; max_pages * page < 2^31  */
+  int32_t max_pages;  /* pages a sequence may have; max_pages * page <= 2^30 */
   int32_t dtype;      /* dtype of K, V, Q, the tail and the output           */
   int32_t code;       /* enum tq_code                                        */
 } tq_paged_desc;
@@ -552,7 +552,7 @@ int tq_paged_init(tq_paged* c, const tq_paged_desc* desc, void* dev_mem, size_t 
  * tq_paged_extend -- take pages for new tokens: row i (0 <= i < n) appends
  * cu[i+1] - cu[i] tokens to slot slots[i]; slot -1 is a padding row whose tokens
  * are left out.  The new tokens become visible at once: write every layer
- * (tq_paged_write) before attending.
+ * (tq_paged_write) before attending and before the next tq_paged_extend.
  *   slots  device int32[n], no slot twice;  cu  device int32[n+1], cu[0] >= 0, not
  *          decreasing
  *   n      1..desc.slots
@@ -600,7 +600,7 @@ int tq_paged_table(const tq_paged* c, const int32_t* slots, int n, int32_t* out,
  *   Hq       a multiple of Hkv, at most 8 Hkv
  *   cu       device int32[n+1], not decreasing; max_q >= every cu[i+1] - cu[i]
  *   total_q  tokens in Q and out; tokens outside [cu[0], cu[n]) are left as they were
- *   out      device [total_q][Hq][d] of desc.dtype (written)
+ *   out      device [total_q][Hq][d] of desc.dtype (written); not over Q
  *   lse      device float[total_q][Hq]: log sum exp of the scaled logits (-inf where
  *            nothing is visible), or NULL
  *   workspace  device, 256-byte aligned, tq_paged_workspace_bytes(c) bytes, made

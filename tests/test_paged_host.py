@@ -47,7 +47,7 @@ def test_layout(nat, page, d, es, dt):
 @pytest.mark.parametrize("kw,status", [
     (dict(d=96), 2), (dict(page=48), 2), (dict(page=256), 2), (dict(code=2), 2), (dict(layers=0), 1),
     (dict(Hkv=0), 1), (dict(pages=0), 1), (dict(pages=(1 << 20) + 1), 1), (dict(slots=0), 1),
-    (dict(slots=65537), 1), (dict(max_pages=0), 1), (dict(max_pages=1 << 25), 2), (dict(dtype=3), 1)])
+    (dict(slots=65537), 1), (dict(max_pages=0), 1), (dict(max_pages=(1 << 24) + 1), 2), (dict(dtype=3), 1)])
 def test_bad_descriptors(nat, kw, status):
     assert nat.tq_paged_bytes(_desc(nat, **kw)) == 0
     with pytest.raises(nat.TQError) as e:
@@ -94,6 +94,8 @@ def test_host_refusals(nat):
                dict(wsp=None), dict(wsp=ODD), dict(wsb=ws - 1)):
         assert attn(**kw) == bad, kw
     assert attn(total=0) == nat.TQ_OK
+    over = ctypes.c_void_p((1 << 20) + 64 * 1024)                             # the output over the queries
+    assert attn(total=9, out=over) == bad and attn(total=9, Q=over, out=FAKE) == bad
     o = nat.tq_paged_layout(_desc(nat, Hkv=4))
     o.base = 1 << 21
     assert L.tq_paged_copy(r, ctypes.byref(o), FAKE, FAKE, 1, S) == bad
