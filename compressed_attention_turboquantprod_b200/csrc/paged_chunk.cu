@@ -54,47 +54,66 @@ template <int ROWS>
 __device__ __forceinline__ int sw_off(int row, int c) {
   return (c >> 3) * (ROWS * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
 }
-// Descriptor of such an operand at shared address `at` (1024-byte aligned), and what k-step k (16
-// f16) adds to it (the start address is its low field, in units of 16 bytes).
+// Descriptor of such an operand at shared address `at` (1024-byte aligned), and what slab k adds to it
+// (the start address is its low field, in units of 16 bytes; a k-step of 16 f16 adds 2).
 __device__ __forceinline__ uint64_t sw_desc(uint32_t at) {
   return (uint64_t)((at >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 template <int ROWS>
-__device__ __forceinline__ constexpr int sw_step(int k) {
-  return (k >> 2) * (ROWS * 8) + (k & 3) * 2;
+__device__ __forceinline__ constexpr int sw_slab(int k) {
+  return k * (ROWS * 8);
 }
 
 // The products' warp runs its loop with all lanes, so that descriptors and addresses stay in uniform
 // registers (in a branch of one thread each product took 200 cycles to issue); one elected lane, always
-// the same, issues each instruction.
-// D[tmem] (+)= A[smem] * B[smem]^T, f16 operands.
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// the same, issues them, four k-steps (one 128-byte slab of the operands) to an election.
+// D[tmem] (+)= A[smem] * B[smem]^T over four k-steps, f16 operands.
+__device__ __forceinline__ void mma4_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem]^T.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem]^T over four k-steps (8 columns of A each).
+__device__ __forceinline__ void mma4_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrive on the mbarrier when every product issued so far has completed.
+// Arrive on the mbarrier when every product issued so far has completed;
+// mma_commit_and_arrive: the issuing lane arrives there itself, too.
 __device__ __forceinline__ void mma_commit_elected(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_and_arrive(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
+      "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
 
@@ -315,19 +334,15 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
 
   if (is_conv) {
     // =================================================================== converters
-    // Warp cw expands tokens cw TW ... of the tile, in halves of 16 that lie in one sub-block.  A warp
-    // instruction takes 8 rows of 4 pieces (keys) or 8 channels of each half (values), so that its 16-byte
-    // stores hit all banks; rows are 128 bytes of the swizzled operand.
-    constexpr int NH = TW / 16;
+    // Warp cw expands tokens 16 cw ... of the tile, which lie in one sub-block.  A warp instruction takes 8
+    // rows of 4 pieces (keys) or a piece of 32 channels (values), so that its 16-byte stores hit all banks;
+    // rows are 128 bytes of the swizzled operand.
     const int cw = warp & 3, l7 = lane & 7, l3 = lane >> 3, par = lane & 1;
-    const int lsub = 31 - __clz(g.sub);
+    const int lsub = 31 - __clz(g.sub), lpage = 31 - __clz(g.page);
     const int64_t vofs = (int64_t)g.Hkv * g.hb;
     const int ko[2] = {D == 64 ? l7 * D + 16 * l3 : l7 * D + 16 * l3 + 64 * par,
                        D == 64 ? 0 : l7 * D + 16 * l3 + 64 * (1 - par)};
-    const int vh = NH == 2 ? l3 & 1 : 0;              // the half and the channel of this lane's value pieces
-    const int vch = NH == 2 ? (lane >> 4) * 8 + l7 : lane;
-    constexpr int VSTEP = NH == 2 ? 16 : 32;
-    const int pc = 2 * (cw * NH + vh);                // their piece along T
+    const int vch = lane, pc = 2 * cw;                // the first channel of this lane's value pieces, their piece along T
     const int kd0 = (cw * TW + l7) * 128 + (((2 * l3) ^ l7) << 4), kd1 = (cw * TW + l7) * 128 + (((2 * l3 + 1) ^ l7) << 4);
     const int vd0 = sw_off<D>(vch, pc), vd1 = sw_off<D>(vch, pc + 1);
     auto put = [&](unsigned char* to, unsigned char* to2, const uint4& v) {        // 16 codes -> two pieces of a row
@@ -344,43 +359,39 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       const int tok0 = sg.first * T + cw * TW, last = cur.s.len - 1;
       const int* table = g.table + (int64_t)cur.s.slot * g.max_pages;
       uint4 kr[NK], vr[NK];
-      int pid[NH], off[NH];                           // page and token offset in it of each half, a tile ahead
-      const uint8_t* kp[NH];
+      int pid, off;                                   // page of the warp's tokens and their offset in it, a tile ahead
+      const uint8_t* kp = nullptr;                    // their key sub-block
+      const uint8_t* heads = g.pool + (int64_t)a.layer * g.pages * g.page_bytes + (int64_t)cur.h * g.hb;
       float sk = 0.f, sv = 0.f;
       auto look = [&](int t) {
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          // past the end: the last sub-block's, masked but finite
-          const int tk = min(tok0 + t * T + 16 * h, last & ~15);
-          pid[h] = table[tk / g.page];
-          off[h] = tk % g.page;
-        }
+        // past the end: the last sub-block's, masked but finite
+        const int tk = min(tok0 + t * T, last & ~15);
+        pid = table[tk >> lpage];
+        off = tk & (g.page - 1);
       };
       auto load_k = [&]() {
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          if ((unsigned)pid[h] >= (unsigned)g.pages) {
-            if (lane == 0) atomicOr(&g.state->status, kPagedBadPage);
-            pid[h] = 0;
-          }
-          kp[h] = paged_block(g, a.layer, pid[h], 0, cur.h, off[h] >> lsub);
-          off[h] &= g.sub - 1;
+        if ((unsigned)pid >= (unsigned)g.pages) {
+          if (lane == 0) atomicOr(&g.state->status, kPagedBadPage);
+          pid = 0;
         }
+        kp = heads + pid * g.page_bytes + (off >> lsub) * g.sb;
+        off &= g.sub - 1;
+        const uint8_t* p0 = kp + off * D;
 #pragma unroll
         for (int it = 0; it < NK; ++it) {
-          const int cg = it % (D / 64), rg = it / (D / 64);          // 8-row group, 64-byte group
-          const uint8_t* p = kp[rg / 2] + off[rg / 2] * D + ko[cg & 1] + (cg >> 1) * 128 + (rg & 1) * 8 * D;
+          const int cg = it % (D / 64), rg = it / (D / 64);          // 64-byte group, 8-row group
+          const uint8_t* p = p0 + ko[cg & 1] + (cg >> 1) * 128 + rg * 8 * D;
           kr[it] = TQ_CHECKED(p, 16, g.base, g.total, 421) ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
         }
-        const uint8_t* tr = (NH == 2 && (lane & 1) ? kp[NH - 1] : kp[0]) + ((int64_t)D << lsub);
+        const uint8_t* tr = kp + (D << lsub);
         sk = *reinterpret_cast<const float*>(tr);
         sv = *reinterpret_cast<const float*>(tr + vofs);
       };
       auto load_v = [&]() {
-        const uint8_t* p = (vh ? kp[NH - 1] + off[NH - 1] : kp[0] + off[0]) + vofs + (vch << lsub);
+        const uint8_t* p = kp + off + vofs + (vch << lsub);
 #pragma unroll
         for (int it = 0; it < NK; ++it) {
-          const uint8_t* q = p + ((it * VSTEP) << lsub);
+          const uint8_t* q = p + ((it * 32) << lsub);
           vr[it] = TQ_CHECKED(q, 16, g.base, g.total, 422) ? *reinterpret_cast<const uint4*>(q) : make_uint4(0, 0, 0, 0);
         }
       };
@@ -394,9 +405,9 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         unsigned char* V = K + 2 * kTb;
         if (n >= 2) wait(&sh.k_free[b2], (n >> 1) - 1);
         // four sets of scales: the products of tile n - 2 are done, so the softmax of tile n - 4 is
-        if (lane < NH) {
-          sh.sk[n & 3][cw * NH + lane] = sk;
-          sh.lv[n & 3][cw * NH + lane] = sv > 0.f ? __log2f(sv) : 0.f;     // a block of zeros: any scale will do
+        if (lane == 0) {
+          sh.sk[n & 3][cw] = sk;
+          sh.lv[n & 3][cw] = sv > 0.f ? __log2f(sv) : 0.f;     // a block of zeros: any scale will do
         }
 #pragma unroll
         for (int it = 0; it < NK; ++it) {
@@ -410,7 +421,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         if (t + 1 < nt) load_k();
         if (n >= 2) wait(&sh.v_free[b2], (n >> 1) - 1);
 #pragma unroll
-        for (int it = 0; it < NK; ++it) put(V + vd0 + it * VSTEP * 128, V + vd1 + it * VSTEP * 128, vr[it]);
+        for (int it = 0; it < NK; ++it) put(V + vd0 + it * 32 * 128, V + vd1 + it * 32 * 128, vr[it]);
         tc::fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.v_full[b2]);
@@ -426,15 +437,12 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
                    dV = sw_desc(__shfl_sync(0xffffffffu, sV, 0));
     auto qk = [&](int w, int b2, int qb) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_ss(tm + cS + (2 * w + b2) * T, dQ + (uint64_t)(qb * (kQb / 16) + w * (128 * D * 2 / 16) + sw_step<128>(k)),
-               dK + (uint64_t)(b2 * (kTb / 16) + sw_step<T>(k)), iS, k > 0);
+      for (int k = 0; k < D / 64; ++k)
+        mma4_ss(tm + cS + (2 * w + b2) * T, dQ + (uint64_t)(qb * (kQb / 16) + w * (128 * D * 2 / 16) + sw_slab<128>(k)),
+                dK + (uint64_t)(b2 * (kTb / 16) + sw_slab<T>(k)), iS, k > 0);
     };
     auto pv = [&](int w, int b2, bool first) {
-#pragma unroll
-      for (int k = 0; k < T / 16; ++k)
-        mma_ts(tm + cO + w * D, tm + cS + (2 * w + b2) * T + 8 * k, dV + (uint64_t)(b2 * (kTb / 16) + sw_step<D>(k)), iO,
-               !(first && k == 0));
+      mma4_ts(tm + cO + w * D, tm + cS + (2 * w + b2) * T, dV + (uint64_t)(b2 * (kTb / 16)), iO, !first);
     };
     walk([&](const auto&, int nt_, int n0_, int seg_) {
       const int nt = __shfl_sync(0xffffffffu, nt_, 0), n0 = __shfl_sync(0xffffffffu, n0_, 0),
@@ -451,8 +459,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
             if (n >= 1) wait(&sh.pv_done[w][m & 1], (n - 1) >> 1);
             tc::fence_after_sync();
             qk(w, m & 1, seg % NQ);
-            mma_commit_elected(&sh.s_full[w][m & 1]);
-            if (lane == 0) mbar_arrive(&sh.s_full[w][m & 1]);
+            mma_commit_and_arrive(&sh.s_full[w][m & 1]);
           }
           mma_commit_elected(&sh.k_free[m & 1]);
         }
