@@ -732,7 +732,8 @@ template <int D>
 cudaError_t chunk_d(const PGeom& g, const PagedAttn& a, cudaStream_t s) {
   const bool i8 = g.code == TQ_CODE_INT8;
   if constexpr (chunk_max_mt<D>() == 2) {
-    // one row block where no sequence has more rows than it holds
+    // one row block where no sequence has more rows than it holds (128 rows over 8 x 32768 tokens, G = 4, d =
+    // 128: 277 us, with two blocks 328; 256 rows: 533 us in ones, 316 in twos)
     if ((int64_t)a.max_q * (a.Hq / g.Hkv) > 128)
       return i8 ? chunk_t<D, TQ_CODE_INT8, 2>(g, a, s) : chunk_t<D, TQ_CODE_E4M3, 2>(g, a, s);
   }
