@@ -197,16 +197,25 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
 
   // ---- queries: warp w brings rows 2 w and 2 w + 1 of a unit, a unit ahead
   constexpr int NQ = D / 32;                // lane l holds channels NQ l .. NQ l + NQ - 1
-  float qn[2][NQ];
+  const bool f32 = g.dtype == TQ_F32, f16 = g.dtype == TQ_F16;
+  uint32_t qn[2][NQ];                       // fp32, or two 16-bit entries a word in the first half of them
   auto bring = [&](const Cursor& u) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int row = u.rg * kDecRows + 2 * warp + j;
       const int64_t tok = (int64_t)u.s.q0 + row / G;
       const bool ok = row < u.s.nq * G && tok >= 0 && tok < a.total_q;
+      const int64_t at = tok * a.q_stride + (int64_t)(u.h * G + row % G) * D + NQ * lane;
 #pragma unroll
-      for (int k = 0; k < NQ; ++k)
-        qn[j][k] = ok ? load_f(a.Q, tok * a.q_stride + (int64_t)(u.h * G + row % G) * D + NQ * lane + k, g.dtype) : 0.f;
+      for (int k = 0; k < NQ; ++k) qn[j][k] = 0;
+      if (ok) {
+        const uint32_t* p = static_cast<const uint32_t*>(a.Q) + (f32 ? at : at >> 1);
+#pragma unroll
+        for (int k = 0; k < NQ / 2; ++k) qn[j][k] = p[k];
+        if (f32)
+#pragma unroll
+          for (int k = NQ / 2; k < NQ; ++k) qn[j][k] = p[k];
+      }
     }
   };
   bring(cur);                               // (their latency passes behind the first requests')
@@ -225,10 +234,16 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
       const int r = 2 * warp + j, row = cur.rg * kDecRows + r;
       const int64_t tok = (int64_t)cur.s.q0 + row / G;
       const bool ok = r < rows && tok >= 0 && tok < a.total_q;
-      float mx = 0.f;
+      float qf[NQ], mx = 0.f;
+#pragma unroll
+      for (int k = 0; k < NQ; k += 2) {
+        const float2 v = f32 ? make_float2(__uint_as_float(qn[j][k]), __uint_as_float(qn[j][k + 1])) : unpack2(qn[j][k / 2], f16);
+        qf[k] = v.x;
+        qf[k + 1] = v.y;
+      }
 #pragma unroll
       for (int k = 0; k < NQ; ++k) {
-        const float t = fabsf(qn[j][k]);
+        const float t = fabsf(qf[k]);
         mx = fmaxf(mx, t <= 3.402823466e38f ? t : 0.f);
       }
       mx = warp_max(mx);
@@ -238,7 +253,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
       __half* A = reinterpret_cast<__half*>(s_q);
 #pragma unroll
       for (int k = 0; k < NQ; ++k) {
-        const float v = qn[j][k] * up;
+        const float v = qf[k] * up;
         const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
         // channel 64 j + 16 c' + 4 w + b is k-step 4 j + w, lane (r, c'), register 2 (b / 2), half b mod 2
         const int ch = NQ * lane + k;
@@ -431,10 +446,16 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
                        a.total_q * a.Hq * D * paged_esize(g.dtype), 402)) {
           const float inv = L > 0.f ? 1.f / L : 0.f;
           const int64_t at = (otok * a.Hq + ohq) * D;
+          if (f32) {
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            store_f(a.out, at + 8 * i + 2 * c, g.dtype, L > 0.f ? o[i][0] * inv : 0.f);
-            store_f(a.out, at + 8 * i + 2 * c + 1, g.dtype, L > 0.f ? o[i][1] * inv : 0.f);
+            for (int i = 0; i < NT; ++i)
+              *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + 8 * i + 2 * c) =
+                  L > 0.f ? make_float2(o[i][0] * inv, o[i][1] * inv) : make_float2(0.f, 0.f);
+          } else {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+              *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at + 8 * i + 2 * c) =
+                  L > 0.f ? pack2(o[i][0] * inv, o[i][1] * inv, f16) : 0u;
           }
           if (a.lse && c == 0) a.lse[otok * a.Hq + ohq] = L > 0.f ? (M + log2f(L)) * (1.f / kLog2e) : -INFINITY;
         }
@@ -484,9 +505,17 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
         const int hq = cur.h * G + row % G;
         if (r < rows && tok >= 0 && tok < a.total_q) {
           const float inv = La > 0.f ? 1.f / La : 0.f;
+          const int64_t at = (tok * a.Hq + hq) * D + 4 * k;
 #pragma unroll
-          for (int q = 0; q < CH; ++q)
-            store_f(a.out, (tok * a.Hq + hq) * D + 64 * (q >> 2) + 4 * k + (q & 3), g.dtype, La > 0.f ? oo[q] * inv : 0.f);
+          for (int q = 0; q < CH; ++q) oo[q] = La > 0.f ? oo[q] * inv : 0.f;
+#pragma unroll
+          for (int q = 0; q < CH; q += 4) {
+            if (f32)
+              *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + 16 * q) = make_float4(oo[q], oo[q + 1], oo[q + 2], oo[q + 3]);
+            else
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + 16 * q) =
+                  make_uint2(pack2(oo[q], oo[q + 1], f16), pack2(oo[q + 2], oo[q + 3], f16));
+          }
           if (a.lse && k == 0) a.lse[tok * a.Hq + hq] = La > 0.f ? (Ma + log2f(La)) * (1.f / kLog2e) : -INFINITY;
         }
       }

@@ -182,17 +182,6 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
   asm volatile("" : "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]) : : "memory");
 }
 
-// Two entries of a model type as floats, and back.
-__device__ __forceinline__ float2 unpack2(uint32_t u, bool f16) {
-  return f16 ? __half22float2(*reinterpret_cast<const __half2*>(&u))
-             : make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b, bool f16) {
-  if (f16) return pack_half(a, b);
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 template <int D, int CODE, int MT>
 __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, PagedAttn a) {
   constexpr int T = kTokens, R = 128 * MT, NTH = R + 256;

@@ -325,5 +325,16 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two entries of a model type as floats, and back.
+__device__ __forceinline__ float2 unpack2(uint32_t u, bool f16) {
+  return f16 ? __half22float2(*reinterpret_cast<const __half2*>(&u))
+             : make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, bool f16) {
+  if (f16) return pack_half(a, b);
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 }  // namespace paged
 }  // namespace tq
