@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
   pdl_wait();
   pdl_launch_dependents();
   const int G = a.Hq / g.Hkv;
+  const DivG by_g(G);
   const uint32_t magic = *static_cast<const volatile uint32_t*>(a.ws);
   const int cta = blockIdx.x;
   Cursor cur;
@@ -203,9 +204,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int row = u.rg * kDecRows + 2 * warp + j;
-      const int64_t tok = (int64_t)u.s.q0 + row / G;
+      const int q = by_g(row);
+      const int64_t tok = (int64_t)u.s.q0 + q;
       const bool ok = row < u.s.nq * G && tok >= 0 && tok < a.total_q;
-      const int64_t at = tok * a.q_stride + (int64_t)(u.h * G + row % G) * D + NQ * lane;
+      const int64_t at = tok * a.q_stride + (u.h * G + row - q * G) * D + NQ * lane;
 #pragma unroll
       for (int k = 0; k < NQ; ++k) qn[j][k] = 0;
       if (ok) {
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int r = 2 * warp + j, row = cur.rg * kDecRows + r;
-      const int64_t tok = (int64_t)cur.s.q0 + row / G;
+      const int64_t tok = (int64_t)cur.s.q0 + by_g(row);
       const bool ok = r < rows && tok >= 0 && tok < a.total_q;
       float qf[NQ], mx = 0.f;
 #pragma unroll
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
       }
       if (lane == 0) {
         s_fr[r] = ok ? a.scale * kLog2e * __int_as_float((127 - e) << 23) : 0.f;
-        s_vis[r] = ok ? visible(cur.s, row / G, a.causal) : 0;
+        s_vis[r] = ok ? visible(cur.s, by_g(row), a.causal) : 0;
       }
     }
     if (xe < x1) {
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
       float sc[8][4];
 #pragma unroll
       for (int i = 0; i < 8; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
-#pragma unroll
+#pragma unroll(D == 256 ? 4 : 1)            // (rolled where it costs nothing: every launch fetches the code anew)
       for (int j = 0; j < D / 64; ++j) {
         uint4 A[4];
 #pragma unroll
@@ -431,8 +433,9 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
       for (int i = 0; i < NT; ++i) so2[i * 32 + lane] = make_float2(o[i][0], o[i][1]);
     __syncthreads();
     const bool whole = x == cur.u0 && xe == ue;
-    const int64_t otok = (int64_t)cur.s.q0 + (cur.rg * kDecRows + gi) / G;
-    const int ohq = cur.h * G + (cur.rg * kDecRows + gi) % G;
+    const int oq = by_g(cur.rg * kDecRows + gi);
+    const int64_t otok = (int64_t)cur.s.q0 + oq;
+    const int ohq = cur.h * G + cur.rg * kDecRows + gi - oq * G;
     if (warp == 0) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
@@ -501,8 +504,8 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
           }
         }
         const int row = cur.rg * kDecRows + r;
-        const int64_t tok = (int64_t)cur.s.q0 + row / G;
-        const int hq = cur.h * G + row % G;
+        const int64_t tok = (int64_t)cur.s.q0 + by_g(row);
+        const int hq = cur.h * G + row - by_g(row) * G;
         if (r < rows && tok >= 0 && tok < a.total_q) {
           const float inv = La > 0.f ? 1.f / La : 0.f;
           const int64_t at = (tok * a.Hq + hq) * D + 4 * k;

@@ -265,9 +265,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
     }
   };
 
-  // row / G for row < 2^27, G <= 8: the reciprocal's error times row stays below 1 / G
-  const uint32_t gm = (uint32_t)(0x100000000ull / (uint32_t)G) + 1u;
-  auto by_g = [&](int row) { return G == 1 ? row : (int)__umulhi((uint32_t)row, gm); };
+  const DivG by_g(G);
   // Place of row i of the unit in an array of tokens `stride` entries apart (a token's heads lie side
   // by side), in entries; -1: none.
   auto place = [&](int i, int64_t stride) {

@@ -21,6 +21,14 @@ constexpr size_t kWsHeader = 4096;
 // share of the list, whatever the lengths: a share may begin and end inside a unit, and then leaves
 // a partial output for the CTA that finishes that unit last.  Lengths are read on the device, so a
 // captured call follows them.
+// row / G for row < 2^27 and G <= 8: the reciprocal's error times row stays below 1 / G.
+struct DivG {
+  int G;
+  uint32_t m;
+  __device__ __forceinline__ explicit DivG(int g) : G(g), m((uint32_t)(0x100000000ull / (uint32_t)g) + 1u) {}
+  __device__ __forceinline__ int operator()(int row) const { return G == 1 ? row : (int)__umulhi((uint32_t)row, m); }
+};
+
 struct Seq {
   int slot, len, nq, q0;
 };
