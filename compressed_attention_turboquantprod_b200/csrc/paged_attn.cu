@@ -30,6 +30,12 @@ constexpr int kTile = 64;
 // 16 c + 2 i + {0, 1}: the 16 tokens whose value bytes are its one 16-byte read per channel.
 // Each tile's P V starts from zero and is added to the fp32 output in round-to-nearest (the
 // tensor core's own long sums truncate: 2^-25 a step, one way).
+//
+// Measured (one B200, copy peak 6466 GB/s): 8 sequences of 32768 tokens, 32 / 8 heads, d = 128, int8:
+// 101 us for 537 MB, 0.82 of the peak, DRAM traffic 1.02 of that; d = 256, e4m3, 223 k tokens of 4 heads:
+// 92 us, 0.77.  One sequence of 517 tokens: 15 us, a chain of about ten dependent loads and the first
+// fetch of the code.  What bounds the long ones is latency within a warp: 8 warps an SM (4 at d = 256) at
+// 44 % issue, as many as 240 registers allow; three CTAs at d = 64 (143 registers) gained nothing.
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecRows = 8;

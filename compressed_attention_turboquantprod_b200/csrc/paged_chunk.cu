@@ -4,7 +4,7 @@
 // A CTA works on R = 128 MT query rows of one KV head (row r: query r / G, head r mod G, so that
 // grouped heads share every tile) and walks its share of their tiles of T tokens:
 //   S_w = Q_w K^T       A = Q_w (128 x D, shared memory), B = K (T x D), fp32 in tensor memory
-//   P_w = 2^(f S_w + log2 s_v - M)      a thread per row, f16 back into tensor memory over S_w
+//   P_w = 2^(f S_w + log2 s_v - M)      a thread per row, f16 back into tensor memory over S_w (two S take turns)
 //   O_w += P_w V        A = P_w (tensor memory), B = V (D x T, shared memory)
 // A warpgroup per row block runs its softmax, four converter warps read the next tile's codes
 // into registers while they expand the last one's into the f16 operands, three warps bring the next
@@ -20,6 +20,15 @@
 // first tile's scale so that it stays in range.  Rounding p to f16 (2^-11 relative, as fine as the
 // output's own rounding) is the one loss beside q's, which is held to 2^-11 of a f16 entry's own
 // bits or exactly (bf16, f16 entries have at most 11 bits; q is scaled by a power of two per row).
+//
+// Measured (one B200, bf16 peak 1644 TFLOP/s): 64 queries on each of 8 x 32768 tokens, 32 / 8 heads, d =
+// 128, int8: 341 us, 806 TFLOP/s; prompts of 8192 and 6001 tokens on themselves, e4m3: 1006 us, 840
+// TFLOP/s.  A tile of 64 tokens takes about 2050 cycles where its products need 1280 and its exponentials
+// 1024.  The limit is the shared issue of 16 warps in four roles, each near its own serial time: leaving out
+// the exponentials, the expansion, the products or the loads alone gains 2, 0, 10 and 7 %, all four together
+// 43 %.  T = 128 with one S a row block took 3.0 ms on the prompts (each softmax waited for its own
+// products), S single and P apart 1.06 ms, products from a branch of one thread 3.2 ms, two converters
+// for the keys and two for the values 1.04 ms, requests into L2 four tiles ahead 1.03 ms.
 #include "paged_split.cuh"
 #include "tc_common.cuh"
 
