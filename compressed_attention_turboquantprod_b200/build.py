@@ -23,7 +23,8 @@ LIB_BOUNDS = os.path.join(PKG, "libtq_bounds.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
-         "-Xcompiler", "-fPIC", "-Xcompiler", "-O3", "-Xcompiler", "-ffp-contract=off", "-shared"]
+         "-Xcompiler", "-fPIC", "-Xcompiler", "-O3", "-Xcompiler", "-ffp-contract=off", "-shared",
+         "--threads", "0"]            # the files are compiled side by side
 
 
 def nvcc() -> str:

@@ -504,3 +504,62 @@ def test_few_rows_of_a_chunk_many_times():
     rows, cu = i32([0, 1]), offsets([10, 20])
     for _ in range(200):
         assert torch.equal(first, c.cross(Q, rows, cu, 20))
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0])
+def test_chunk_with_a_negative_and_a_zero_scale(scale):
+    c, m = make(1, 64, 20, 1, 20, 32, "int8", "bf16")
+    fill(c, m, [150], "bf16", 111)
+    Q = tokens(40, 4, 64, "bf16", 112, 0.3)
+    check_attention(c, m, Q, [0], [40], True, "bf16", scale=scale, single_p=True)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (256, 128)])
+def test_what_a_page_held_before_does_not_show(code, d, page):
+    """Pages of freed sequences with entries near the type's largest, infinities and NaN are taken by
+    short ones: the places behind a sequence's end hold those codes still."""
+    c, m = make(1, d, 8, 2, 8, page, code, "bf16")
+    big = tokens(8 * page, 1, d, "bf16", 121) * 1e36
+    big[::7] = float("inf")
+    big[3::11] = float("nan")
+    c.append(big, big, i32([0]), offsets([8 * page]))
+    c.free(i32([0]))
+    fill(c, m, [page // 2 + 1, 1], "bf16", 122)
+    same_values(c, m, "bf16")
+    Q = tokens(2, 3, d, "bf16", 123, 0.3)
+    check_attention(c, m, Q, [0, 1], [1, 1], True, "bf16")
+    Q = tokens(41, 3, d, "bf16", 124, 0.3)
+    check_attention(c, m, Q, [0, 1], [40, 1], False, "bf16", single_p=True)
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 4 GB: the last layer's pages lie past 2^32 bytes."""
+    c, m = make(8, 128, 700, 2, 10, 64, "int8", "bf16", layers=56)
+    assert c.state.o_pool + 55 * 700 * c.state.page_bytes > 2 ** 32
+    counts = [130, 3]
+    c.extend(i32([0, 1]), offsets(counts))
+    K, V = tokens(133, 8, 128, "bf16", 131), tokens(133, 8, 128, "bf16", 132)
+    c.write(K, V, layer=55)
+    k, v = (op.cached_values(host(t[:130]), "int8", 64) for t in (K, V))
+    rk, rv = c.read(i32([0]), offsets([130]), 130, layer=55)
+    for got, want in ((rk, k), (rv, v)):
+        assert (np.abs(host(got) - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -23) + 1e-30).all()
+    assert (c.read(i32([0]), offsets([130]), 130, layer=54)[0] == 0).all()
+    Q = tokens(41, 16, 128, "bf16", 133, 0.3)
+    want, _, mass, reach = op.attention(host(Q), k, v, True, 128 ** -0.5)
+    for got, lo, p_step in ((c.attend(Q, i32([0]), offsets([41]), 41, layer=55), 0, 2.0 ** -11),
+                            (c.decode(Q[40:].contiguous(), i32([0]), layer=55), 40, 0.0)):
+        ew = (2 * (128 + 8) * 2.0 ** -24 * reach[lo:] + 2.0 ** -19 + p_step)[..., None] * mass[lo:]
+        tol = 2.0 ** -36 * 130 * np.abs(v).max() + ew + 2.0 ** -8 * (np.abs(want[lo:]) + ew)
+        assert (np.abs(host(got) - want[lo:]) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("G,nq", [(8, 3), (4, 5), (1, 24), (5, 4), (1, 25), (8, 4)])
+def test_few_queries_on_either_side_of_the_rule(dtype, G, nq):
+    """9 to 32 query rows of a KV head: several groups of 8 rows, a group that holds rows of two queries."""
+    c, m = make(2, 128, 60, 2, 30, 32, "e4m3", dtype)
+    fill(c, m, [500, nq + 1], dtype, 141)
+    Q = tokens(2 * nq, 2 * G, 128, dtype, 142, 0.3)
+    check_attention(c, m, Q, [0, 1], [nq, nq], True, dtype, single_p=nq * G > 24)
