@@ -241,7 +241,7 @@ class PagedKVCache:
     def _on(self, *tensors):
         """The cache's device made current; every tensor of the call has to be on it."""
         for t in tensors:
-            if t is not None and t.device != self.buffer.device:
+            if t is not None and t.get_device() != self._index:
                 raise ValueError(f"tensor on {t.device}, the cache is on {self.buffer.device}")
         if torch.cuda.current_device() == self._index:
             return _CURRENT

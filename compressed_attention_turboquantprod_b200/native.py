@@ -170,10 +170,17 @@ def raw_stream(device: int) -> int:
     return _raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
 
 
-def _stream_fast(stream) -> ctypes.c_void_p:
-    if stream is None:
-        return ctypes.c_void_p(raw_stream(torch.cuda.current_device()))
-    return _stream(stream)
+def _stream_fast(stream):
+    return raw_stream(torch.cuda.current_device()) if stream is None else _stream(stream)
+
+
+def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
+    """_ptr as a plain integer (what the paged calls pass; no ctypes object a tensor)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    return t.data_ptr()
 
 
 def dtype_code(dt: torch.dtype) -> int:
@@ -382,12 +389,12 @@ def tq_paged_layout(desc: tq_paged_desc) -> tq_paged:
 
 
 def tq_paged_init(cache: tq_paged, desc: tq_paged_desc, buf: torch.Tensor, stream=None):
-    _check(lib.tq_paged_init(ctypes.byref(cache), ctypes.byref(desc), _ptr(buf),
+    _check(lib.tq_paged_init(ctypes.byref(cache), ctypes.byref(desc), _addr(buf),
                              buf.numel() * buf.element_size(), _stream_fast(stream)), "tq_paged_init")
 
 
 def _tokens(t: torch.Tensor, heads: int, d: int):
-    """(pointer, token stride in elements) of a token-major [tokens, heads, d] tensor whose
+    """(address, token stride in elements) of a token-major [tokens, heads, d] tensor whose
     tokens are contiguous (a view into a wider row, such as a fused projection, will do)."""
     if t.dim() != 3 or t.shape[1:] != (heads, d):
         raise ValueError(f"expected [tokens, {heads}, {d}], got {tuple(t.shape)}")
@@ -400,7 +407,7 @@ def _tokens(t: torch.Tensor, heads: int, d: int):
 def _i32(t: torch.Tensor):
     if t.dtype != torch.int32 or t.dim() != 1:
         raise ValueError("slots and offsets are one-dimensional int32 tensors")
-    return _ptr(t)
+    return _addr(t)
 
 
 def _rows(slots: torch.Tensor, cu: torch.Tensor) -> int:
@@ -424,11 +431,11 @@ def tq_paged_write(cache: tq_paged, layer: int, K, V, stream=None):
 
 def tq_paged_read(cache: tq_paged, layer: int, slots, cu, K, V, stream=None):
     _check(lib.tq_paged_read(ctypes.byref(cache), layer, _i32(slots), _i32(cu), _rows(slots, cu),
-                             K.shape[0], _ptr(K), _ptr(V), _stream_fast(stream)), "tq_paged_read")
+                             K.shape[0], _addr(K), _addr(V), _stream_fast(stream)), "tq_paged_read")
 
 
 def tq_paged_table(cache: tq_paged, slots, out, stream=None):
-    _check(lib.tq_paged_table(ctypes.byref(cache), _i32(slots), slots.numel(), _ptr(out),
+    _check(lib.tq_paged_table(ctypes.byref(cache), _i32(slots), slots.numel(), _addr(out),
                               _stream_fast(stream)), "tq_paged_table")
 
 
@@ -437,7 +444,7 @@ def tq_paged_workspace_bytes(cache: tq_paged) -> int:
 
 
 def tq_paged_workspace_init(cache: tq_paged, workspace, stream=None):
-    _check(lib.tq_paged_workspace_init(ctypes.byref(cache), _ptr(workspace), _ws(workspace),
+    _check(lib.tq_paged_workspace_init(ctypes.byref(cache), _addr(workspace), _ws(workspace),
                                        _stream_fast(stream)), "tq_paged_workspace_init")
 
 
@@ -448,7 +455,7 @@ def tq_paged_attention(cache: tq_paged, layer: int, Q, slots, cu, max_q: int, ca
     qp, qs = _tokens(Q, Hq, cache.desc.d)
     _check(lib.tq_paged_attention(ctypes.byref(cache), layer, qp, qs, Hq, _i32(slots), _i32(cu),
                                   _rows(slots, cu), max_q, Q.shape[0], int(causal), softmax_scale,
-                                  _ptr(out), _ptr(lse), _ptr(workspace), _ws(workspace),
+                                  _addr(out), _addr(lse), _addr(workspace), _ws(workspace),
                                   _stream_fast(stream)), "tq_paged_attention")
 
 
