@@ -354,8 +354,16 @@ __global__ void __launch_bounds__(kPlanThreads, 1) k_paged_compact(PGeom g) {
 
 // ---------------------------------------------------------------- moving bytes
 __device__ __forceinline__ void copy16(uint8_t* to, const uint8_t* from, int64_t bytes) {
-  for (int64_t o = 16 * (int64_t)threadIdx.x; o < bytes; o += 16 * kMoveThreads)
-    *reinterpret_cast<uint4*>(to + o) = *reinterpret_cast<const uint4*>(from + o);
+  // four reads in flight a thread
+  int64_t o = 16 * (int64_t)threadIdx.x;
+  for (; o + 3 * 16 * kMoveThreads < bytes; o += 4 * 16 * kMoveThreads) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(from + o + k * 16 * kMoveThreads);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(to + o + k * 16 * kMoveThreads) = v[k];
+  }
+  for (; o < bytes; o += 16 * kMoveThreads) *reinterpret_cast<uint4*>(to + o) = *reinterpret_cast<const uint4*>(from + o);
 }
 
 // The moves of the last plan, in all layers; then, for a fork or copy, the exact tails and
@@ -449,13 +457,13 @@ cudaError_t paged_launch_branch(const PGeom& src, const PGeom& dst, const int* f
                                 bool share, cudaStream_t s) {
   cudaError_t e = launch_pdl(k_paged_branch, dim3(1), dim3(kPlanThreads), 0, s, src, dst, from, to, n, (int)share);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_paged_move, dim3(148 * 8), dim3(kMoveThreads), 0, s, src, dst, from, to, (int)share);
+  return launch_pdl(k_paged_move, dim3(148 * 4), dim3(kMoveThreads), 0, s, src, dst, from, to, (int)share);
 }
 
 cudaError_t paged_launch_compact(const PGeom& g, cudaStream_t s) {
   cudaError_t e = launch_pdl(k_paged_compact, dim3(1), dim3(kPlanThreads), 0, s, g);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_paged_move, dim3(148 * 8), dim3(kMoveThreads), 0, s, g, g, (const int*)nullptr,
+  return launch_pdl(k_paged_move, dim3(148 * 4), dim3(kMoveThreads), 0, s, g, g, (const int*)nullptr,
                     (const int*)nullptr, 0);
 }
 
