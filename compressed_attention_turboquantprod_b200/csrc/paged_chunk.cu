@@ -26,7 +26,7 @@
 // TFLOP/s.  A tile of 64 tokens takes about 2050 cycles where its products need 1280 and its exponentials
 // 1024.  The limit is the shared issue of 16 warps in four roles, each near its own serial time: leaving out
 // the exponentials, the expansion, the products or the loads alone gains 2, 0, 10 and 7 %, all four together
-// 43 %.  T = 128 with one S a row block took 3.0 ms on the prompts (each softmax waited for its own
+// 43 %.  Tried in the states of the time: T = 128 with one S a row block took 3.0 ms on the prompts (each softmax waited for its own
 // products), S single and P apart 1.06 ms, products from a branch of one thread 3.2 ms, two converters
 // for the keys and two for the values 1.04 ms, requests into L2 four tiles ahead 1.03 ms.
 #include "paged_split.cuh"

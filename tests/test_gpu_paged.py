@@ -563,3 +563,40 @@ def test_few_queries_on_either_side_of_the_rule(dtype, G, nq):
     fill(c, m, [500, nq + 1], dtype, 141)
     Q = tokens(2 * nq, 2 * G, 128, dtype, 142, 0.3)
     check_attention(c, m, Q, [0, 1], [nq, nq], True, dtype, single_p=nq * G > 24)
+
+
+def test_the_largest_batch_and_pool():
+    """65536 sequences in a pool of 2^20 pages: plans over many rounds, a compaction of the whole pool."""
+    n = 65536
+    c, _ = make(1, 64, 1 << 20, n, 4, 16, "int8", "f16")
+    rows = torch.arange(n, dtype=torch.int32, device="cuda")
+    counts = rows % 37
+    cu = torch.cat([counts.new_zeros(1), counts.cumsum(0).int()])
+    total = int(cu[-1])
+    x = tokens(total, 1, 64, "f16", 151)
+    c.append(x, x, rows, cu)
+    assert torch.equal(c.lengths, counts)
+    used = (counts + 15) // 16
+    table = c.page_table(rows)
+    have = torch.arange(4, device="cuda") < used[:, None]
+    assert torch.equal(table[have], torch.arange(int(used.sum()), dtype=torch.int32, device="cuda"))
+    assert (table[~have] == -1).all()
+    K, _ = c.read(rows, cu, total)
+    err = (K.float() - x.float()).abs()                  # at most half a step of the block's scale, and the type's
+    assert float((err - x.float().abs().max() / 254 - x.float().abs() * 2.0 ** -11).max()) <= 0
+    c.free(rows[: n // 2])
+    c.compact()
+    live = int(used[n // 2:].sum())
+    assert c.check() == (1 << 20) - live
+    table = c.page_table(rows)[n // 2:]
+    got = table[have[n // 2:]]
+    assert torch.equal(got.sort().values, torch.arange(live, dtype=torch.int32, device="cuda"))
+    again, _ = c.read(rows[n // 2:], cu[n // 2:] - cu[n // 2], total - int(cu[n // 2]))
+    assert torch.equal(again, K[int(cu[n // 2]):])
+    q = tokens(n // 2, 2, 64, "f16", 152)
+    out = c.decode(q, rows[n // 2:])
+    assert torch.isfinite(out.float()).all() and (out[counts[n // 2:] == 0] == 0).all()
+    one = counts[n // 2:] == 1                           # a single token: its value, rounded once more at most
+    at = (cu[n // 2:-1] - cu[n // 2])[one].long()
+    v = again[at][:, 0].float()                          # (K and V got the same tokens)
+    assert ((out[one].float() - v[:, None]).abs() <= 2.0 ** -10 * v.abs()[:, None] + 2.0 ** -24).all()
