@@ -45,6 +45,12 @@ constexpr float kSlack = 4.f;
 
 constexpr int kTokens = 64;                // tokens of a tile
 constexpr int kUnitCost = 8;               // places of a unit besides its tiles (16k cycles, 2k a tile)
+// The tensor core's fp32 sums truncate: a row of O loses up to 2^-23 of itself, always towards zero, with
+// every k-step of 16 tokens (measured 1e-7 a step: 0.7 % after 2^20 tokens).  So O is added, rounded to
+// nearest, to a sum in the workspace and begun anew after this many tiles: 8192 tokens, 512 steps, 2^-14 at
+// most, an eighth of what rounding p to f16 may cost.  64 queries on 8 x 32768 tokens (shares of 222 tiles):
+// 342 us, without folding 344, folded after 64 tiles 366 (three folds in place of one).
+constexpr int kFold = 128;
 template <int D>
 __host__ __device__ constexpr int chunk_max_mt() { return D == 256 ? 1 : 2; }
 // Query operands: this unit's and the next one's, where they fit.
@@ -124,6 +130,12 @@ __device__ __forceinline__ void mma_commit_and_arrive(uint64_t* bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
       "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
+}
+
+// *p += v, rounded to nearest, without waiting.
+__device__ __forceinline__ void red_add4(float4* p, const float4& v) {
+  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
 }
 
 struct ChunkWs {
@@ -466,7 +478,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
             wait(&sh.p_ready[w][n & 1], n >> 1);
             if (t == 0 && seg > 0) wait(&sh.o_free[w], seg - 1);      // the last unit's O has been read
             tc::fence_after_sync();
-            pv(w, n & 1, t == 0);
+            pv(w, n & 1, t % kFold == 0);
             mma_commit_elected(&sh.pv_done[w][n & 1]);
           }
           mma_commit_elected(&sh.v_free[n & 1]);
@@ -485,6 +497,16 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       const bool ok = place(r, 0) >= 0;
       const int vis = ok ? visible(cur.s, by_g(row0 + r), a.causal) : 0;
       float fr = 0.f, M = kNone, l = 0.f, lvr = 0.f;
+      // The sum that O is folded into, for the reference Mf: the row's place in the segment's part.  (A unit
+      // that this CTA holds alone uses the part of the unit that goes on after it, which is written last.)
+      const int slot = 2 * cta + (sg.first == 0 ? 1 : 0);
+      float4* part = reinterpret_cast<float4*>(ws.o + (int64_t)slot * R * D) + r;      // [D / 4][R]
+      float Mf = kNone;
+      auto folded = [&](int i, float w) {              // channels 4 i ... of that sum, times w
+        const float4* from = &part[(int64_t)i * R];
+        const float4 v = TQ_CHECKED(from, 16, a.ws, (int64_t)a.ws_bytes, 425) ? __ldcg(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+        return make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
+      };
       unsigned char* Q = smem + (seg % NQ) * kQb + (size_t)wg * 128 * D * 2;  // the row block's operand, later its output
       if (nt > 0) {
         if (seg == 0) {
@@ -543,12 +565,42 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
                                max3(max3(S(9), S(10), S(11)), S(12), S(13)), fmaxf(S(14), S(15)));
           zmax = fmaxf(zmax, m == -INFINITY ? m : fmaf(m, f[h], lv[h]));
         }
+        if (t > 0 && t % kFold == 0) {                 // (P V of this tile begins O anew)
+          pv_wait(n - 1);
+          tc::fence_after_sync();
+          // the first O as it is; later ones added where they lie (nothing is waited for), unless a
+          // row's reference has moved on since
+          const int how = t == kFold ? 0 : __all_sync(0xffffffffu, Mf == M) ? 1 : 2;
+          const float w = ex2(Mf - M);
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(tO + 16 * c, o);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float4* to = &part[(int64_t)(4 * c + k) * R];
+              if (!TQ_CHECKED(to, 16, a.ws, (int64_t)a.ws_bytes, 426)) continue;
+              float4 v = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                     __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+              if (how == 1) {
+                red_add4(to, v);
+                continue;
+              }
+              if (how == 2) {
+                const float4 u = __ldcg(to);
+                v = make_float4(fmaf(u.x, w, v.x), fmaf(u.y, w, v.y), fmaf(u.z, w, v.z), fmaf(u.w, w, v.w));
+              }
+              *to = v;
+            }
+          }
+          Mf = M;
+        }
         if (__any_sync(0xffffffffu, M == kNone ? zmax > -INFINITY : zmax > M + kSlack)) {
           const float Mn = M == kNone ? (zmax == -INFINITY ? kNone : zmax) : fmaxf(M, zmax);
           const float alpha = M == kNone ? 0.f : ex2(M - Mn);
           M = Mn;
           l *= alpha;
-          if (t > 0) {
+          if (t % kFold != 0) {
             pv_wait(n - 1);
             tc::fence_after_sync();
 #pragma unroll 1
@@ -597,7 +649,6 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       const float inv = l > 0.f ? ex2(lvr) / l : 0.f;
       const float lse2 = l > 0.f ? log2f(l) + (M - lvr - kBias) : -INFINITY;
       const int64_t lse_at = ((int64_t)cur.s.q0 + by_g(row0 + r)) * a.Hq + cur.h * G + row0 + r - by_g(row0 + r) * G;
-      const int slot = 2 * cta + (sg.first == 0 ? 1 : 0);
       if (nt > 0) {
         pv_wait(n0 + nt - 1);                          // (and so the row block's products with Q are done)
         tc::fence_after_sync();
@@ -615,12 +666,21 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         }
         __syncwarp();
       };
-      float4* part = reinterpret_cast<float4*>(ws.o + (int64_t)slot * R * D) + r;      // [D / 4][R]
+      const float wf = ex2(Mf - M);
 #pragma unroll 1
       for (int c = 0; c < D / 32 && nt > 0; ++c) {
         uint32_t v[32];
         tc::tmem_ld32(tO + 32 * c, v);
         tmem_wait_ld(v);
+        if (nt > kFold)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 s = folded(8 * c + i, wf);
+            v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + s.x);
+            v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + s.y);
+            v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + s.z);
+            v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + s.w);
+          }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float o[8];

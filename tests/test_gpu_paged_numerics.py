@@ -1,0 +1,85 @@
+"""What the paged cache's attention must not lose: long sums, value scales far apart (a block of zeros
+among them), queries that are not finite, and what a mask hides.
+
+The bounds are those of test_gpu_paged.py, taken over what a query sees: with p at most 1 against the
+running maximum and b a visible block's largest |v|, a half keeps p b off by at most 2^-36 (chunks of bf16
+and f16, against the largest p b in sight) or 2^-40 (decode, against the largest b in sight)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import TORCH_DT, host
+from oracle import paged as op
+from test_gpu_paged import HALF, TINY, i32, make, offsets, tokens
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(q, k, v, b, vis, scale):
+    """One query [d] over its first `vis` tokens of one head, in float64; b: the largest |v| of each
+    token's block.  (out, lse, sum p |v|, largest scale sum |q k|, largest p b, largest b)."""
+    s = scale * (k[:vis] @ q)
+    m = s.max()
+    p = np.exp(s - m)
+    l = p.sum()
+    reach = (abs(scale) * (np.abs(k[:vis]) @ np.abs(q))).max()
+    return p @ v[:vis] / l, m + math.log(l), p @ np.abs(v[:vis]) / l, reach, (p * b[:vis]).max() / l, b[:vis].max() / l
+
+
+def check(c, page, K, V, Q, causal, dtype, scale=None, single_p=True, code="int8"):
+    """Q over slot 0, which holds K and V, against the oracle; returns the output."""
+    n, Hq, d = Q.shape
+    Hkv, T, G = K.shape[1], K.shape[0], Hq // K.shape[1]
+    sc = 1.0 / math.sqrt(d) if scale is None else scale
+    lse = torch.full((n, Hq), 7.0, device="cuda")
+    got = c.attend(Q, i32([0]), offsets([n]), n, causal, sc, lse=lse)
+    c.check()
+    k, v = (op.cached_values(host(t), code, page) for t in (K, V))
+    b = np.zeros((T, Hkv))
+    for t in range(0, T, page):
+        b[t:t + page] = np.abs(v[t:t + page]).max(axis=(0, 2))
+    q64, g64, l64 = host(Q), host(got), lse.cpu().double().numpy()
+    for i in range(n):
+        vis = max(0, min(T, T - n + i + 1)) if causal else T
+        for h in range(Hq):
+            if vis == 0:
+                assert (g64[i, h] == 0).all() and np.isneginf(l64[i, h])
+                continue
+            want, wl, mass, reach, pb, bb = reference(q64[i, h], k[:, h // G], v[:, h // G], b[:, h // G], vis, sc)
+            ew = 2 * (d + 8) * 2.0 ** -24 * reach + 2.0 ** -19 + (2.0 ** -11 if single_p else 0.0)
+            floor = vis * (2.0 ** -36 * pb if single_p else 2.0 ** -40 * bb)
+            tol = floor + ew * mass + HALF[dtype] * (np.abs(want) + ew * mass) + TINY[dtype]
+            err = np.abs(g64[i, h] - want)
+            assert (err <= tol).all(), (i, h, vis, float((err / tol).max()), float(err.max()))
+            assert abs(l64[i, h] - wl) <= ew + 2.0 ** -22 * (1 + abs(wl)), (i, h, l64[i, h], wl)
+    return got
+
+
+@pytest.mark.parametrize("d,G,rows", [(64, 1, 148), (64, 1, 100), (128, 8, 148), (256, 2, 148)])
+def test_chunk_sums_of_a_long_sequence(d, G, rows):
+    """Values around 1 over 400001 tokens: a sum that always rounds the same way would drift by 2^-24 of
+    itself a step of 16 tokens (25000 of them).  Many rows name the one sequence, so that a CTA sums most
+    or all of it.  Bound: p's rounding (2^-11), at most 512 steps that truncate (2^-23 each) before they are
+    folded, a rounding for each of the folds (2^-24, at most 400) and for each joined part."""
+    T, n, page = 400001, 26, 64
+    c, _ = make(1, d, T // page + 2, 1, T // page + 1, page, "int8", "f16")
+    g = torch.Generator().manual_seed(7)
+    K = torch.randn(T, 1, d, generator=g).half()
+    V = (1.0 + 0.25 * torch.randn(T, 1, d, generator=g)).half()
+    c.append(K.cuda(), V.cuda(), i32([0]), offsets([T]))
+    Q = tokens(n, G, d, "f16", 8, 0.3)
+    got = c.cross(Q.repeat(rows, 1, 1), i32([0] * rows), offsets([n] * rows), n)
+    c.check()
+    k, v = (torch.from_numpy(op.cached_values(host(t), "int8", page)).cuda()[:, 0] for t in (K, V))
+    q = Q.double().reshape(n * G, d)
+    p = torch.softmax(q @ k.T / math.sqrt(d), -1)
+    want, mass = p @ v, p @ v.abs()
+    reach = (q.abs() @ k.abs().T).max() / math.sqrt(d)
+    ew = float(2 * (d + 8) * 2.0 ** -24 * reach + 2.0 ** -19 + 2.0 ** -11 + 512 * 2.0 ** -23 + 410 * 2.0 ** -24)
+    tol = ew * mass + 2.0 ** -11 * (want.abs() + ew * mass)
+    err = (got.double().reshape(rows, n * G, d) - want).abs()
+    assert float((err / tol).max()) <= 1, (float((err / tol).max()), float(err.max()))
+
+
