@@ -16,8 +16,11 @@
 // factor f (one per 16 tokens), its value scale is added to the exponent, so that O sums code
 // products only.  M is a running reference of f S + log2 s_v, raised only when a tile passes it by
 // more than 2^4 (O is rescaled then); p is at most 2^15, and p <= 2^11 when M is fresh.  The
-// weights' sum, taken in fp32 before p is rounded to f16, divides s_v out again, against the
-// first tile's scale so that it stays in range.  Rounding p to f16 (2^-11 relative, as fine as the
+// weights' sum l, taken in fp32 before p is rounded to f16, is held against a reference R of f S alone:
+// a weight is p 2^(M - R - 11 - log2 s_v), a factor per 16 tokens.  While the value scales in sight lie in
+// 2^-60 .. 2^40 (every f16 scale does), M - R does too, and p and the factor stay in fp32's range.  Tiles
+// with a scale outside, those behind them, and tiles with a block of zero values, which has no scale and
+// must not enter M, take their weights from the logits instead.  Rounding p to f16 (2^-11 relative, as fine as the
 // output's own rounding) is the one loss beside q's, which is held to 2^-11 of a f16 entry's own
 // bits or exactly (bf16, f16 entries have at most 11 bits; q is scaled by a power of two per row).
 //
@@ -41,6 +44,8 @@ constexpr int kConv = 4;                   // converter warps
 constexpr int kLoad = 3;                   // query warps
 constexpr float kNone = -1e30f;            // reference of a row that has seen no token
 constexpr float kBias = 11.f;              // p is held times 2^11
+constexpr float kScaleLo = -60.f, kScaleHi = 40.f;    // log2 s_v of ordinary tiles
+constexpr float kZeros = -3e38f;           // log2 s_v of a block of zeros: below any M, kNone too
 constexpr float kSlack = 4.f;
 
 constexpr int kTokens = 64;                // tokens of a tile
@@ -158,7 +163,7 @@ struct ChunkShared {
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], q_free[2], o_free[2];
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];      // [row block][tile mod 2]
   SplitPlan plan;
-  float sk[4][4], lv[4][4];                // a tile's scales per 16 tokens: of the keys, log2 of the values'
+  float sk[4][4], lv[4][4];                // a tile's scales per 16 tokens: of the keys, log2 of the values' (or kZeros)
   float fr[2][128 * MT];                   // a row's factor on S, per query operand
   Cursor cur;
   uint32_t tmem;
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         // four sets of scales: the products of tile n - 2 are done, so the softmax of tile n - 4 is
         if (lane == 0) {
           sh.sk[n & 3][cw] = sk;
-          sh.lv[n & 3][cw] = sv > 0.f ? __log2f(sv) : 0.f;     // a block of zeros: any scale will do
+          sh.lv[n & 3][cw] = sv > 0.f ? __log2f(sv) : kZeros;
         }
 #pragma unroll
         for (int it = 0; it < NK; ++it) {
@@ -496,7 +501,8 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       const int row0 = cur.rg * R;                     // the CTA's first row of the sequence (below 2^27)
       const bool ok = place(r, 0) >= 0;
       const int vis = ok ? visible(cur.s, by_g(row0 + r), a.causal) : 0;
-      float fr = 0.f, M = kNone, l = 0.f, lvr = 0.f;
+      float fr = 0.f, M = kNone, l = 0.f, Rw = kNone;
+      bool far = false;                                // a scale has been out of range in this segment
       // The sum that O is folded into, for the reference Mf: the row's place in the segment's part.  (A unit
       // that this CTA holds alone uses the part of the unit that goes on after it, which is written last.)
       const int slot = 2 * cta + (sg.first == 0 ? 1 : 0);
@@ -537,7 +543,6 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       if (nt > 0) {
         wait(&sh.s_full[wg][n0 & 1], n0 >> 1);
         tc::fence_after_sync();
-        lvr = sh.lv[n0 & 3][0];
         tc::tmem_ld32(s_at(n0), v[0]);
         tc::tmem_ld32(s_at(n0) + 32, v[1]);
       }
@@ -563,8 +568,10 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
           auto S = [&](int i) { return __uint_as_float(v[h >> 1][16 * (h & 1) + i]); };
           const float m = max3(max3(max3(S(0), S(1), S(2)), max3(S(3), S(4), S(5)), max3(S(6), S(7), S(8))),
                                max3(max3(S(9), S(10), S(11)), S(12), S(13)), fmaxf(S(14), S(15)));
-          zmax = fmaxf(zmax, m == -INFINITY ? m : fmaf(m, f[h], lv[h]));
+          zmax = fmaxf(zmax, fmaf(m, f[h], lv[h]));    // (nothing visible and f = 0: NaN, which fmaxf drops)
         }
+        const float top = fmaxf(fmaxf(lv[0], lv[1]), fmaxf(lv[2], lv[3]));
+        const bool odd = far || top > kScaleHi || fminf(fminf(lv[0], lv[1]), fminf(lv[2], lv[3])) < kScaleLo;
         if (t > 0 && t % kFold == 0) {                 // (P V of this tile begins O anew)
           pv_wait(n - 1);
           tc::fence_after_sync();
@@ -595,22 +602,52 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
           }
           Mf = M;
         }
-        if (__any_sync(0xffffffffu, M == kNone ? zmax > -INFINITY : zmax > M + kSlack)) {
-          const float Mn = M == kNone ? (zmax == -INFINITY ? kNone : zmax) : fmaxf(M, zmax);
-          const float alpha = M == kNone ? 0.f : ex2(M - Mn);
-          M = Mn;
-          l *= alpha;
-          if (t % kFold != 0) {
-            pv_wait(n - 1);
-            tc::fence_after_sync();
+        const bool raise = __any_sync(0xffffffffu, zmax > M + kSlack);
+        float e0 = M - Rw - kBias;                     // p to weight: 2^(e0 - log2 s_v)
+        if (raise || odd) {
+          if (raise) {
+            const float Mn = fmaxf(M, zmax);
+            const float alpha = ex2(M - Mn);           // (M = kNone: 0, or 1 of nothing)
+            M = Mn;
+            // R never passes the largest f S: that of M's token is at least M less the tile's largest scale
+            const float Rn = fmaxf(Rw, M - top);
+            l *= ex2(Rw - Rn);
+            Rw = Rn;
+            if (t % kFold != 0) {
+              pv_wait(n - 1);
+              tc::fence_after_sync();
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(tO + 16 * c, o);
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(tO + 16 * c, o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st16(tO + 16 * c, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st16(tO + 16 * c, o);
+              }
             }
+            e0 = M - Rw - kBias;
+          }
+          if (odd) {
+#pragma unroll
+            for (int h = 0; h < T / 16; ++h) far = far || lv[h] > kScaleHi || (lv[h] < kScaleLo && lv[h] != kZeros);
+            // rare, so in little code: S once more from tensor memory, 16 tokens at a time
+#pragma unroll 1
+            for (int h = 0; h < T / 16; ++h) {
+              uint32_t u[16];
+              tmem_ld16(tS + 16 * h, u);
+              const float ff = fr * sh.sk[sc][h];
+              float x[16], hi = Rw;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                x[i] = base + 16 * h + i < vis ? __uint_as_float(u[i]) * ff : -INFINITY;
+                hi = fmaxf(hi, x[i]);
+              }
+              l *= ex2(Rw - hi);
+              Rw = hi;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) l += ex2(x[i] - Rw);
+            }
+            e0 = -INFINITY;                            // they are counted
           }
         }
         // p and its sum.  A masked S is -inf: its product with f = 0 (an unused row, a block of
@@ -631,7 +668,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
               ls = add2(ls, p);
               pk[8 * e + i] = pack_half(p.x, p.y);
             }
-            l = fmaf(ls.x + ls.y, ex2(lvr - lv[h]), l);
+            l = fmaf(ls.x + ls.y, ex2(e0 - lv[h]), l);
           }
           tmem_st16(tS + 16 * c, pk);
           if (t + 1 < nt) {
@@ -646,8 +683,8 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       if (nt > 0) hand_over(n0 + nt - 1);
       // ---- the row's output, or its part
       const bool whole = sg.whole(cur);
-      const float inv = l > 0.f ? ex2(lvr) / l : 0.f;
-      const float lse2 = l > 0.f ? log2f(l) + (M - lvr - kBias) : -INFINITY;
+      const float inv = l > 0.f ? 1.f / l : 0.f, up = ex2(M - Rw - kBias);
+      const float lse2 = l > 0.f ? log2f(l) + Rw : -INFINITY;
       const int64_t lse_at = ((int64_t)cur.s.q0 + by_g(row0 + r)) * a.Hq + cur.h * G + row0 + r - by_g(row0 + r) * G;
       if (nt > 0) {
         pv_wait(n0 + nt - 1);                          // (and so the row block's products with Q are done)
@@ -685,7 +722,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         for (int i = 0; i < 4; ++i) {
           float o[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] = l > 0.f ? __uint_as_float(v[8 * i + k]) * inv : 0.f;
+          for (int k = 0; k < 8; ++k) o[k] = l > 0.f ? __uint_as_float(v[8 * i + k]) * inv * up : 0.f;
           if (whole) {
             *reinterpret_cast<uint4*>(Q + sw_off<128>(r & 127, 4 * c + i)) =
                 make_uint4(pack2(o[0], o[1], f16), pack2(o[2], o[3], f16), pack2(o[4], o[5], f16), pack2(o[6], o[7], f16));

@@ -83,3 +83,57 @@ def test_chunk_sums_of_a_long_sequence(d, G, rows):
     assert float((err / tol).max()) <= 1, (float((err / tol).max()), float(err.max()))
 
 
+@pytest.mark.parametrize("where", ["before", "between", "after", "all"])
+@pytest.mark.parametrize("d,page,code", [(64, 16, "int8"), (128, 64, "e4m3"), (256, 128, "int8"), (128, 32, "int8")])
+@pytest.mark.parametrize("size", [1.0, 1e-4, 1e-8])
+def test_chunk_with_blocks_of_zero_values(where, d, page, code, size):
+    """Padding tokens with values of zero: they take their weight and nothing else."""
+    T = 4 * page + 150
+    K, V = tokens(T, 1, d, "bf16", 11), size * tokens(T, 1, d, "bf16", 12)
+    lo, hi = {"before": (0, 2 * page), "between": (page, 3 * page), "after": (3 * page, T), "all": (0, T)}[where]
+    V[lo:hi] = 0
+    c, _ = make(1, d, 40, 1, 40, page, code, "bf16")
+    c.append(K, V, i32([0]), offsets([T]))
+    for causal in (True, False):
+        check(c, page, K, V, tokens(33, 3, d, "bf16", 13, 0.3), causal, "bf16", code=code)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_chunk_with_value_scales_far_apart(page):
+    """Pages 2^40 apart, as the decode takes them; causal rows that see the small ones only."""
+    T = 700
+    K, V = tokens(T, 1, 128, "bf16", 21), tokens(T, 1, 128, "bf16", 22)
+    V[128:192] *= 2.0 ** -20
+    V[640:] *= 2.0 ** 20
+    K[256:320] *= 2.0 ** -20
+    c, _ = make(1, 128, 60, 1, 60, page, "int8", "bf16")
+    c.append(K, V, i32([0]), offsets([T]))
+    check(c, page, K, V, tokens(100, 2, 128, "bf16", 23, 0.3), True, "bf16")
+    check(c, page, K, V, tokens(30, 2, 128, "bf16", 24, 0.3), False, "bf16")
+
+
+@pytest.mark.parametrize("order", [(120, -95), (-95, 120), (0, 120), (120, 0), (0, -95), (-95, 0), (-95, -95)])
+@pytest.mark.parametrize("heavy", [False, True])
+@pytest.mark.parametrize("split", [False, True])
+def test_chunk_over_the_whole_range_of_value_scales(order, heavy, split):
+    """Values of 2^a in the first pages and 2^b in the last, zeros between; heavy: the larger ones get no
+    weight (logits 300 below), so that the smaller ones decide the output.  split: over several CTAs."""
+    page, d = 64, 64
+    T = (40 if split else 6) * page
+    third = T // 3 // page * page
+    K, V = tokens(T, 1, d, "bf16", 31, 0.1), tokens(T, 1, d, "bf16", 32, 0.1)
+    V = V.clamp(-8, 8)
+    V[:third] *= 2.0 ** order[0]
+    V[third:2 * third] = 0
+    V[2 * third:] *= 2.0 ** order[1]
+    Q = tokens(50, 1, d, "bf16", 33, 0.1)
+    if heavy:
+        big = slice(0, third) if order[0] > order[1] else slice(2 * third, T)
+        K[..., 0], Q[..., 0] = 0, 8
+        K[big][..., 0] = -300.0
+    c, _ = make(1, d, 50, 1, 50, page, "int8", "bf16")
+    c.append(K, V, i32([0]), offsets([T]))
+    check(c, page, K, V, Q, False, "bf16", scale=0.125)
+    check(c, page, K, V, Q, True, "bf16", scale=0.125)
+
+
