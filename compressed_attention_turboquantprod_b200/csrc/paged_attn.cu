@@ -453,20 +453,22 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
         if (gi < rows && otok >= 0 && otok < a.total_q &&
             TQ_CHECKED(static_cast<char*>(a.out) + (otok * a.Hq + ohq) * D * paged_esize(g.dtype), D * paged_esize(g.dtype), a.out,
                        a.total_q * a.Hq * D * paged_esize(g.dtype), 402)) {
-          const float inv = L > 0.f ? 1.f / L : 0.f;
+          // only a row that sees nothing gives 0: a NaN in L, from a query that is not finite, is passed on
+          const bool none = vis == 0;
+          const float inv = 1.f / L;
           const int64_t at = (otok * a.Hq + ohq) * D;
           if (f32) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
               *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + 8 * i + 2 * c) =
-                  L > 0.f ? make_float2(o[i][0] * inv, o[i][1] * inv) : make_float2(0.f, 0.f);
+                  none ? make_float2(0.f, 0.f) : make_float2(o[i][0] * inv, o[i][1] * inv);
           } else {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
               *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at + 8 * i + 2 * c) =
-                  L > 0.f ? pack2(o[i][0] * inv, o[i][1] * inv, f16) : 0u;
+                  none ? 0u : pack2(o[i][0] * inv, o[i][1] * inv, f16);
           }
-          if (a.lse && c == 0) a.lse[otok * a.Hq + ohq] = L > 0.f ? (M + log2f(L)) * (1.f / kLog2e) : -INFINITY;
+          if (a.lse && c == 0) a.lse[otok * a.Hq + ohq] = none ? -INFINITY : (M + log2f(L)) * (1.f / kLog2e);
         }
       } else {
         const int slot = 2 * cta + (x == cur.u0 ? 1 : 0);
@@ -513,10 +515,11 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
         const int64_t tok = (int64_t)cur.s.q0 + by_g(row);
         const int hq = cur.h * G + row - by_g(row) * G;
         if (r < rows && tok >= 0 && tok < a.total_q) {
-          const float inv = La > 0.f ? 1.f / La : 0.f;
+          const bool none = s_vis[r] == 0;
+          const float inv = 1.f / La;
           const int64_t at = (tok * a.Hq + hq) * D + 4 * k;
 #pragma unroll
-          for (int q = 0; q < CH; ++q) oo[q] = La > 0.f ? oo[q] * inv : 0.f;
+          for (int q = 0; q < CH; ++q) oo[q] = none ? 0.f : oo[q] * inv;
 #pragma unroll
           for (int q = 0; q < CH; q += 4) {
             if (f32)
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
               *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + 16 * q) =
                   make_uint2(pack2(oo[q], oo[q + 1], f16), pack2(oo[q + 2], oo[q + 3], f16));
           }
-          if (a.lse && k == 0) a.lse[tok * a.Hq + hq] = La > 0.f ? (Ma + log2f(La)) * (1.f / kLog2e) : -INFINITY;
+          if (a.lse && k == 0) a.lse[tok * a.Hq + hq] = none ? -INFINITY : (Ma + log2f(La)) * (1.f / kLog2e);
         }
       }
     }

@@ -606,11 +606,12 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         float e0 = M - Rw - kBias;                     // p to weight: 2^(e0 - log2 s_v)
         if (raise || odd) {
           if (raise) {
-            const float Mn = fmaxf(M, zmax);
+            // each row by itself: what it gives must not depend on the rows that share its warp
+            const float Mn = zmax > M + kSlack ? zmax : M;
             const float alpha = ex2(M - Mn);           // (M = kNone: 0, or 1 of nothing)
             M = Mn;
             // R never passes the largest f S: that of M's token is at least M less the tile's largest scale
-            const float Rn = fmaxf(Rw, M - top);
+            const float Rn = alpha == 1.f ? Rw : fmaxf(Rw, M - top);
             l *= ex2(Rw - Rn);
             Rw = Rn;
             if (t % kFold != 0) {
@@ -683,8 +684,11 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
       if (nt > 0) hand_over(n0 + nt - 1);
       // ---- the row's output, or its part
       const bool whole = sg.whole(cur);
-      const float inv = l > 0.f ? 1.f / l : 0.f, up = ex2(M - Rw - kBias);
-      const float lse2 = l > 0.f ? log2f(l) + Rw : -INFINITY;
+      // Only a row that sees nothing (of a part: whose weights are all 0) gives 0: a NaN in l, from a query
+      // that is not finite, is passed on.
+      const bool none = whole ? vis == 0 : l == 0.f;
+      const float inv = 1.f / l, up = ex2(M - Rw - kBias);
+      const float lse2 = none ? -INFINITY : log2f(l) + Rw;
       const int64_t lse_at = ((int64_t)cur.s.q0 + by_g(row0 + r)) * a.Hq + cur.h * G + row0 + r - by_g(row0 + r) * G;
       if (nt > 0) {
         pv_wait(n0 + nt - 1);                          // (and so the row block's products with Q are done)
@@ -722,7 +726,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         for (int i = 0; i < 4; ++i) {
           float o[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] = l > 0.f ? __uint_as_float(v[8 * i + k]) * inv * up : 0.f;
+          for (int k = 0; k < 8; ++k) o[k] = none ? 0.f : __uint_as_float(v[8 * i + k]) * inv * up;
           if (whole) {
             *reinterpret_cast<uint4*>(Q + sw_off<128>(r & 127, 4 * c + i)) =
                 make_uint4(pack2(o[0], o[1], f16), pack2(o[2], o[3], f16), pack2(o[4], o[5], f16), pack2(o[6], o[7], f16));
@@ -753,7 +757,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
           for (int p = c0; p <= c1; ++p) m = fmaxf(m, __ldcg(&ws.lse[slot_of(p) * R + r]));
           const float mu = m == -INFINITY ? 0.f : m;
           for (int p = c0; p <= c1; ++p) L += ex2(__ldcg(&ws.lse[slot_of(p) * R + r]) - mu);
-          const float iL = L > 0.f ? 1.f / L : 0.f;
+          const float iL = vis == 0 ? 0.f : 1.f / L;
           // 32 channels at a time: eight reads in flight per part
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -784,7 +788,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
           rows_out();
           if (ok && a.lse)
             a.lse[lse_at] =
-                L > 0.f ? (m + log2f(L)) * (1.f / kLog2e) : -INFINITY;
+                vis == 0 ? -INFINITY : (m + log2f(L)) * (1.f / kLog2e);
         }
       }
       if (nt > 0) {

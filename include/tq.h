@@ -594,7 +594,8 @@ int tq_paged_table(const tq_paged* c, const int32_t* slots, int n, int32_t* out,
  *   causal == 0: every query sees all L tokens (cross attention: the sequence holds
  *                an encoder's states, of a length of its own)
  * out = sum_t p_t v_t, p = softmax(softmax_scale <q, k_t>) over the visible tokens;
- * a query that sees none gives 0.  One query per sequence is the decode.
+ * a query that sees none gives 0, one with a NaN or an infinity gives NaN (and a NaN
+ * lse).  One query per sequence is the decode.
  *   Q        device, token t's heads [Hq][d] at element t * q_stride (16-byte
  *            aligned tokens, q_stride >= Hq * d), of desc.dtype
  *   Hq       a multiple of Hkv, at most 8 Hkv

@@ -137,3 +137,29 @@ def test_chunk_over_the_whole_range_of_value_scales(order, heavy, split):
     check(c, page, K, V, Q, True, "bf16", scale=0.125)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n", [2, 40])
+@pytest.mark.parametrize("T", [100, 6000])
+def test_queries_that_are_not_finite(dtype, n, T):
+    """A NaN or an infinity in a query gives NaN in that query's output and lse and nowhere else, in
+    both kernels and in units of one CTA (100 tokens) or of several (6000); a query that sees nothing gives 0."""
+    c, _ = make(1, 64, 120, 2, 100, 64, "int8", dtype)
+    c.append(tokens(T, 1, 64, dtype, 41), tokens(T, 1, 64, dtype, 42), i32([0]), offsets([T]))
+    Q = tokens(2 * n, 2, 64, dtype, 43, 0.3)
+    rows, cu = i32([0, 1]), offsets([n, n])            # slot 1 is empty
+    lse = [torch.zeros(2 * n, 2, device="cuda") for _ in range(2)]
+    good = c.cross(Q, rows, cu, n, lse=lse[0])
+    for value in (float("nan"), float("inf"), float("-inf")):
+        bad = Q.clone()
+        bad[0, 1, 5] = value
+        bad[n - 1, 0, :] = value
+        bad[n, 0, 3] = value
+        out = c.cross(bad, rows, cu, n, lse=lse[1])
+        hit = torch.zeros(2 * n, 2, dtype=torch.bool, device="cuda")
+        hit[0, 1] = hit[n - 1, 0] = True
+        assert torch.isnan(out[hit]).all() and torch.isnan(lse[1][hit]).all()
+        assert torch.equal(out[~hit], good[~hit]) and torch.equal(lse[1][~hit], lse[0][~hit])
+        assert (out[n:] == 0).all() and torch.isneginf(lse[1][n:]).all()
+    c.check()
+
+
