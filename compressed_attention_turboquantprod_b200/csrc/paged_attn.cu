@@ -351,9 +351,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
           ls += p[i][e];
         }
       l = l * alpha + ls;
-      // ---- P V: p times its page's scale against the tile's largest, split into two halves
+      // ---- P V: p times its page's scale against the largest of those the row sees, split into two halves
       wait_stage();
-      const float sv = *reinterpret_cast<const float*>(ring + cst * STB + 16 * c / SUB * SS + SUB * D);
+      float sv = *reinterpret_cast<const float*>(ring + cst * STB + 16 * c / SUB * SS + SUB * D);
+      if (NSUB > 1 && t0 >= vis) sv = 0.f;
       float st = sv;
       if constexpr (NSUB > 1) {
         st = fmaxf(st, __shfl_xor_sync(0xffffffffu, st, 1));

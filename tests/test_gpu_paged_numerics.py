@@ -163,3 +163,15 @@ def test_queries_that_are_not_finite(dtype, n, T):
     c.check()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("page", [16, 32])
+def test_what_a_mask_hides_does_not_coarsen_the_rest(dtype, page):
+    """Two queries over a page of values near 1e-8 and a token of 1e8 behind it, which only the last one sees."""
+    T = page + 1
+    K, V = tokens(T, 1, 64, dtype, 51), 1e-8 * tokens(T, 1, 64, dtype, 52)
+    V[page] = 1e8
+    c, _ = make(1, 64, 8, 1, 8, page, "int8", dtype)
+    c.append(K, V, i32([0]), offsets([T]))
+    check(c, page, K, V, tokens(2, 2, 64, dtype, 53, 0.3), True, dtype, single_p=False)
+
+
