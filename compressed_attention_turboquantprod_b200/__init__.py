@@ -272,10 +272,15 @@ class PagedKVCache:
         return ws
 
     # ---- tokens in, floats out
-    def extend(self, slots: torch.Tensor, cu: torch.Tensor):
-        """Take pages for cu[i+1]-cu[i] new tokens of each slot; then write() every layer."""
+    def extend(self, slots: torch.Tensor, cu: torch.Tensor, total: Optional[int] = None):
+        """Take pages for cu[i+1]-cu[i] new tokens of each slot; then write() every layer.  total:
+        the tokens that write() will be given, so that offsets past them are refused here, where
+        the cache stays as it was (in write() they store zeros)."""
         with self._on(slots, cu):
-            native.tq_paged_extend(self.state, slots, cu)
+            if total is None:
+                native.tq_paged_extend(self.state, slots, cu)
+            else:
+                native.tq_paged_extend_within(self.state, slots, cu, total)
 
     def write(self, K: torch.Tensor, V: torch.Tensor, layer: int = 0):
         """The tokens of the last extend(), quantised into `layer`."""
@@ -289,7 +294,7 @@ class PagedKVCache:
             raise ValueError("a cache of several layers takes extend() and a write() per layer")
         self._typed(K, V)
         with self._on(K, V, slots, cu):
-            native.tq_paged_extend(self.state, slots, cu)
+            native.tq_paged_extend_within(self.state, slots, cu, K.shape[0])
             native.tq_paged_write(self.state, 0, K, V)
 
     def read(self, slots: torch.Tensor, cu: torch.Tensor, total: int, layer: int = 0):

@@ -41,6 +41,7 @@ struct PagedState {
   int n_pairs;     // pairs of the last fork / copy
   int compacted;   // 1: the last plan renumbers pages (compact)
   int low;         // every page below this one is in use
+  int end;         // input tokens that the last extend's plan reaches to
 };
 
 struct PagedRow {  // one row of an extend: `count` tokens from row `src` of the input
@@ -105,7 +106,8 @@ cudaError_t paged_allow_smem(size_t bytes) {
 
 // ---- host launchers ----
 cudaError_t paged_launch_init(const PGeom& g, cudaStream_t s);      // every slot empty, every page free
-cudaError_t paged_launch_extend(const PGeom& g, const int* slots, const int* cu, int n, cudaStream_t s);
+// total: input tokens there are (the plan is refused if a row goes past them), or -1: not known yet
+cudaError_t paged_launch_extend(const PGeom& g, const int* slots, const int* cu, int n, int64_t total, cudaStream_t s);
 cudaError_t paged_launch_write(const PGeom& g, int layer, const void* K, const void* V, int64_t k_stride,
                                int64_t v_stride, int64_t total, int n_rows, cudaStream_t s);
 cudaError_t paged_launch_read(const PGeom& g, int layer, const int* slots, const int* cu, int n,

@@ -134,6 +134,16 @@ tq::PGeom geom(const tq_paged* c) {
   return g;
 }
 
+int extend(tq_paged* c, const int32_t* slots, const int32_t* cu, int n, int64_t total, void* stream, const char* name) {
+  int st = check(c, name);
+  if (st == TQ_OK) st = check_ints(slots, cu, n, c->desc.slots, name);
+  if (st == TQ_OK) st = check_pending(name);
+  if (st != TQ_OK) return st;
+  const cudaError_t e = tq::paged_launch_extend(geom(c), slots, cu, n, total, static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) c->plan_rows = n;
+  return done(e, name);
+}
+
 // A token stride in elements: whole 16-byte pieces, no token inside another.
 bool bad_stride(const tq_paged* c, int64_t stride, int64_t heads) {
   return stride < heads * c->desc.d || stride * tq::paged_esize(c->desc.dtype) % 16 != 0;
@@ -176,13 +186,14 @@ int tq_paged_init(tq_paged* c, const tq_paged_desc* desc, void* dev_mem, size_t 
 
 int tq_paged_extend(tq_paged* c, const int32_t* slots, const int32_t* cu, int n, void* stream) {
   TQ_FAULT_POINT("tq_paged_extend");
-  int st = check(c, "tq_paged_extend");
-  if (st == TQ_OK) st = check_ints(slots, cu, n, c->desc.slots, "tq_paged_extend");
-  if (st == TQ_OK) st = check_pending("tq_paged_extend");
-  if (st != TQ_OK) return st;
-  const cudaError_t e = tq::paged_launch_extend(geom(c), slots, cu, n, static_cast<cudaStream_t>(stream));
-  if (e == cudaSuccess) c->plan_rows = n;
-  return done(e, "tq_paged_extend");
+  return extend(c, slots, cu, n, -1, stream, "tq_paged_extend");
+}
+
+int tq_paged_extend_within(tq_paged* c, const int32_t* slots, const int32_t* cu, int n, int64_t total, void* stream) {
+  TQ_FAULT_POINT("tq_paged_extend_within");
+  if (total < 0 || total > INT_MAX)
+    return set_error(TQ_ERR_INVALID_ARG, "tq_paged_extend_within: total=%lld", (long long)total);
+  return extend(c, slots, cu, n, total, stream, "tq_paged_extend_within");
 }
 
 int tq_paged_write(const tq_paged* c, int layer, const void* K, const void* V, int64_t k_stride, int64_t v_stride,

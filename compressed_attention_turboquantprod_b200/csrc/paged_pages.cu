@@ -103,11 +103,13 @@ __global__ void k_paged_init(PGeom g) {
 
 // ---------------------------------------------------------------- extend
 // Row i appends cu[i + 1] - cu[i] tokens to slot slots[i] (slot -1: its tokens are left
-// out).  All or nothing: any error sets a status bit and the plan stays empty.
-__global__ void __launch_bounds__(kPlanThreads, 1) k_paged_extend(PGeom g, const int* slots, const int* cu, int n) {
+// out).  All or nothing: any error, a row past the `total` input tokens (-1: not known) among them,
+// sets a status bit and the plan stays empty.
+__global__ void __launch_bounds__(kPlanThreads, 1) k_paged_extend(PGeom g, const int* slots, const int* cu, int n,
+                                                                  int64_t total) {
   __shared__ int s_scan[32];
   __shared__ unsigned long long s_scan2[32];
-  __shared__ int s_bad, s_need, s_items;
+  __shared__ int s_bad, s_need, s_items, s_end;
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x;
@@ -115,6 +117,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) k_paged_extend(PGeom g, const
     s_bad = 0;
     s_need = 0;
     s_items = 0;
+    s_end = 0;
     g.state->n_rows = 0;
     g.state->n_items = 0;
   }
@@ -136,12 +139,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) k_paged_extend(PGeom g, const
         const int64_t end = (int64_t)start + count;
         if (end > (int64_t)g.max_pages * g.page) {
           bad |= kPagedTooLong;
+        } else if (count > 0 && total >= 0 && b > total) {
+          bad |= kPagedBadOffsets;
         } else if (count > 0) {
           const int first = start / g.page, stop = (int)((end + g.page - 1) / g.page);
           // held below 2^20 + 2 (the most pages a pool has), so that sums over 1024 rows
           // stay in 32 bits; a need past the pool's size is refused below
           need = min(stop - (start + g.page - 1) / g.page, g.pages + 1);
           items = min(stop - first, g.pages + 2);
+          atomicMax(&s_end, b);
         }
       }
       if (bad) count = 0;
@@ -188,6 +194,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) k_paged_extend(PGeom g, const
   if (tid == 0) {
     g.state->n_rows = n;
     g.state->n_items = s_items;
+    g.state->end = s_end;
   }
 }
 
@@ -445,8 +452,8 @@ cudaError_t paged_launch_init(const PGeom& g, cudaStream_t s) {
   return e != cudaSuccess ? e : launch_pdl(k_paged_init, dim3(1), dim3(kPlanThreads), 0, s, g);
 }
 
-cudaError_t paged_launch_extend(const PGeom& g, const int* slots, const int* cu, int n, cudaStream_t s) {
-  return launch_pdl(k_paged_extend, dim3(1), dim3(kPlanThreads), 0, s, g, slots, cu, n);
+cudaError_t paged_launch_extend(const PGeom& g, const int* slots, const int* cu, int n, int64_t total, cudaStream_t s) {
+  return launch_pdl(k_paged_extend, dim3(1), dim3(kPlanThreads), 0, s, g, slots, cu, n, total);
 }
 
 cudaError_t paged_launch_free(const PGeom& g, const int* slots, int n, cudaStream_t s) {

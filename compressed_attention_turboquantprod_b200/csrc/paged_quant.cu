@@ -152,12 +152,47 @@ __device__ __forceinline__ float cta_max(float v, float* s) {
   return r;
 }
 
+// A plan that the write cannot serve (it reaches past the input, or was made for more rows than this
+// launch): its tokens are stored as zeros, so that nothing of a page's former owner is left in their places.
+template <int D, int CODE>
+__device__ __noinline__ void write_zeros(const PGeom& g, int layer, int h, int kv, int n_items, int n_rows) {
+  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+    int lo = 0, hi = n_rows;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (g.rows[mid].item <= item) lo = mid; else hi = mid;
+    }
+    const PagedRow row = g.rows[lo];
+    const int p = row.start / g.page + (item - row.item), t0 = p * g.page, end = row.start + row.count;
+    const int n0 = max(row.start, t0) - t0, n1 = min(end, t0 + g.page) - t0;
+    if (n1 <= n0) continue;
+    const int pid = g.table[(int64_t)row.slot * g.max_pages + p];
+    if ((unsigned)pid >= (unsigned)g.pages) {
+      if (threadIdx.x == 0) atomicOr(&g.state->status, kPagedBadPage);
+      continue;
+    }
+    uint8_t* blk = paged_block(g, layer, pid, kv, h, 0);
+    uint8_t* tail = paged_tail(g, layer, row.slot, kv, h);
+    const int es = paged_esize(g.dtype);
+    if (!TQ_CHECKED(blk, g.hb, g.base, g.total, 437) || !TQ_CHECKED(tail, g.tail_head, g.base, g.total, 438)) continue;
+    for (int i = threadIdx.x; i < (n1 - n0) * D; i += kWThreads) {
+      const int t = n0 + i / D, j = i % D, tb = t % g.sub;
+      blk[(int64_t)(t / g.sub) * g.sb + (kv ? j * g.sub + tb : paged_k_off(D, tb, j))] = CODE == TQ_CODE_INT8 ? 128 : 0;
+    }
+    if (n0 == 0 && threadIdx.x < g.page / g.sub)
+      *reinterpret_cast<float2*>(blk + (int64_t)threadIdx.x * g.sb + (int64_t)g.sub * D) = make_float2(0.f, 0.f);
+    if (p == end / g.page)                                             // the page that stays open
+      for (int i = threadIdx.x; i < (n1 - n0) * D * es / 4; i += kWThreads)
+        reinterpret_cast<uint32_t*>(tail + (int64_t)n0 * D * es)[i] = 0;
+  }
+}
+
 // One CTA per (page of the plan, head, K / V): the page's new tokens come once from the
 // input into shared memory, where their largest magnitude is formed and from where they
 // are encoded; codes leave as 16-byte words.  Measured: 32.8 k tokens of 8 heads, d = 128, bf16 to int8: 78 us
 // for 201 MB (0.40 of the copy peak, 49 % issue at 9 CTAs an SM; 12 of them, with spills, took 86 us).
 template <typename T, int D, int CODE>
-__global__ void __launch_bounds__(kWThreads) k_paged_write(PGeom g, int layer, const T* K, const T* V, int64_t k_stride,
+__global__ void __launch_bounds__(kWThreads) k_paged_write(const __grid_constant__ PGeom g, int layer, const T* K, const T* V, int64_t k_stride,
                                                            int64_t v_stride, int64_t total, int max_rows) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float s_red[kWThreads / 32];
@@ -168,6 +203,11 @@ __global__ void __launch_bounds__(kWThreads) k_paged_write(PGeom g, int layer, c
   // the row whose items hold this one: up to 32 rows by one load each, more by bisection
   const int n_items = g.state->n_items, n_rows = g.state->n_rows, lane = tid & 31;
   PagedRow row = g.rows[lane < max_rows ? lane : 0];
+  if (g.state->end > total || n_rows > max_rows) {
+    if (tid == 0 && item < n_items) atomicOr(&g.state->status, kPagedBadOffsets);
+    write_zeros<D, CODE>(g, layer, h, kv, n_items, n_rows);
+    return;
+  }
   if (item >= n_items) return;
   if (n_rows <= 32) {
     const unsigned below = __ballot_sync(0xffffffffu, lane < n_rows && row.item <= item);
@@ -195,10 +235,6 @@ __global__ void __launch_bounds__(kWThreads) k_paged_write(PGeom g, int layer, c
     return;
   }
   const int64_t src0 = (int64_t)row.src + (t0 + n0 - row.start);    // input token of page token n0
-  if (src0 + (n1 - n0) > total) {                                    // offsets past the arrays
-    if (tid == 0) atomicOr(&g.state->status, kPagedBadOffsets);
-    return;
-  }
   constexpr int CH = D * (int)sizeof(T) / 16;      // 16-byte pieces of a token
   constexpr int EP = 16 / (int)sizeof(T);
   T* S = reinterpret_cast<T*>(smem);               // [page][D]
@@ -263,7 +299,7 @@ __global__ void __launch_bounds__(kWThreads) k_paged_write(PGeom g, int layer, c
     const int kept = end % g.page;
     for (int i = tid; i < kept * CH; i += kWThreads) {
       const int64_t t = (int64_t)row.src + row.count - kept + i / CH;
-      if (t < total) tail[i] = *reinterpret_cast<const uint4*>(in + t * stride + (int64_t)h * D + (i % CH) * EP);
+      tail[i] = *reinterpret_cast<const uint4*>(in + t * stride + (int64_t)h * D + (i % CH) * EP);
     }
   }
   const BlockScale b = block_scale(a, g.code);

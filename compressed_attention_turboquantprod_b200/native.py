@@ -120,6 +120,7 @@ def _load() -> ctypes.CDLL:
         "tq_paged_layout": (I, [GD, G]),
         "tq_paged_init": (I, [G, GD, P, SZ, P]),
         "tq_paged_extend": (I, [G, P, P, I, P]),
+        "tq_paged_extend_within": (I, [G, P, P, I, I64, P]),
         "tq_paged_write": (I, [G, I, P, P, I64, I64, I64, P]),
         "tq_paged_read": (I, [G, I, P, P, I, I64, P, P, P]),
         "tq_paged_table": (I, [G, P, I, P, P]),
@@ -419,6 +420,11 @@ def _rows(slots: torch.Tensor, cu: torch.Tensor) -> int:
 def tq_paged_extend(cache: tq_paged, slots, cu, stream=None):
     _check(lib.tq_paged_extend(ctypes.byref(cache), _i32(slots), _i32(cu), _rows(slots, cu),
                                _stream_fast(stream)), "tq_paged_extend")
+
+
+def tq_paged_extend_within(cache: tq_paged, slots, cu, total: int, stream=None):
+    _check(lib.tq_paged_extend_within(ctypes.byref(cache), _i32(slots), _i32(cu), _rows(slots, cu),
+                                      total, _stream_fast(stream)), "tq_paged_extend_within")
 
 
 def tq_paged_write(cache: tq_paged, layer: int, K, V, stream=None):

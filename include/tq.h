@@ -503,8 +503,8 @@ int tq_decode_attention_noalloc(const tq_cache* c, const void* Q, int Hq, float 
  * the caller's buffer on the device: no call needs the host to know a length, and
  * every call can be captured into a CUDA graph and replayed.  What only the device
  * can check (free pages, slots, offsets) is checked there: a call that fails such
- * a check leaves the cache as it was (tq_paged_write then writes nothing), sets a
- * sticky status and goes on; tq_paged_check reads it.
+ * a check leaves the cache as it was (a tq_paged_write behind a failed extend writes
+ * nothing), sets a sticky status and goes on; tq_paged_check reads it.
  * Calls that change a cache must be ordered with each other and with its readers
  * (one stream, or events); readers may overlap, each with its own workspace.
  * Several layers share the page table: tq_paged_extend once, then tq_paged_write
@@ -559,16 +559,25 @@ int tq_paged_init(tq_paged* c, const tq_paged_desc* desc, void* dev_mem, size_t 
  * Device checks: CAPACITY (free pages; max_pages), INVALID_ARG (slots, offsets).
  * Errors: INVALID_ARG, CUDA.
  *
+ * tq_paged_extend_within -- the same for tokens that lie in arrays of `total` tokens
+ * (0 .. 2^31-1): a row of tokens past them is refused with the rest, INVALID_ARG.  A call
+ * that knows its arrays uses this one: tq_paged_write learns their size too late to
+ * leave the cache as it was.
+ *
  * tq_paged_write -- quantise the tokens of the last tq_paged_extend into layer
  * `layer`: row i's tokens are K[cu[i]] .. K[cu[i+1]-1].
  *   K, V     device [total][Hkv][d] of desc.dtype, token-major; token t starts at
  *            element t * k_stride (v_stride), a multiple of 16 bytes and at least
  *            Hkv * d (views into a fused projection need no copy)
  *   total    tokens in K and V (0: nothing to do)
- * Device checks: INVALID_ARG (an offset past `total`; that block is not written).
+ * Device checks: INVALID_ARG (the last plan reaches past `total`, or has more rows than
+ * the one that was last extended from the host when this call was made or captured: all
+ * of the plan's tokens are then stored as zeros).
  * Errors: INVALID_ARG, CUDA.
  */
 int tq_paged_extend(tq_paged* c, const int32_t* slots, const int32_t* cu, int n, void* stream);
+int tq_paged_extend_within(tq_paged* c, const int32_t* slots, const int32_t* cu, int n, int64_t total,
+                           void* stream);
 int tq_paged_write(const tq_paged* c, int layer, const void* K, const void* V, int64_t k_stride,
                    int64_t v_stride, int64_t total, void* stream);
 

@@ -1,0 +1,109 @@
+"""Calls on the paged cache that are refused, or that come in an order or at a time that other tests do
+not try: what they leave behind."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import host, nat
+from test_gpu_paged import check_attention, fill, i32, make, offsets, same_tables, same_values, tokens
+
+pytestmark = pytest.mark.gpu
+
+
+def dirty(c, m, dtype):
+    """Every page and tail filled with large values of a sequence that is gone."""
+    n = min(c.desc.pages // c.desc.slots, c.desc.max_pages) * c.desc.page
+    big = 1e3 + tokens(n * c.desc.slots, m.Hkv, m.d, dtype, 900)
+    slots = i32(range(c.desc.slots))
+    c.extend(slots, offsets([n] * c.desc.slots))
+    for l in range(m.layers):
+        c.write(big, big, layer=l)
+    c.free(slots)
+    c.check()
+
+
+def refused(c, m, dtype, status, call):
+    from compressed_attention_turboquantprod_b200 import TQError
+    call()
+    with pytest.raises(TQError) as e:
+        c.check()
+    assert e.value.status == status
+    same_tables(c, m)
+    for l in range(m.layers):
+        same_values(c, m, dtype, layer=l)
+
+
+@pytest.mark.parametrize("code,page", [("int8", 16), ("e4m3", 64)])
+def test_an_append_past_its_tokens_is_refused_whole(code, page):
+    bad = nat().TQ_ERR_INVALID_ARG
+    c, m = make(2, 64, 32, 4, 8, page, code, "f16")
+    dirty(c, m, "f16")
+    fill(c, m, [20, 16], "f16", 71)
+    K = tokens(80, 2, 64, "f16", 72)
+    for given, rows, cu in ((3, [3], [0, 9]), (0, [3], [0, 9]), (0, [0], [0, 1]), (3, [0, 3], [0, 2, 4]),
+                            (3, [2, 0, 1], [1, 2, 3, 60]), (9, [0], [9, 10])):
+        refused(c, m, "f16", bad, lambda: c.append(K[:given], K[:given], i32(rows), i32(cu)))
+    # past the tokens, but of no row: padding, and a row without tokens
+    c.append(K[:3], K[:3], i32([0, -1, 1]), i32([0, 3, 50, 50]))
+    m.append(0, [(host(K[:3]), host(K[:3]))])
+    same_tables(c, m)
+    same_values(c, m, "f16")
+
+
+def test_an_extend_that_knows_its_tokens_is_refused_whole():
+    n = nat()
+    c, m = make(1, 128, 20, 3, 8, 32, "int8", "bf16", layers=2)
+    dirty(c, m, "bf16")
+    fill(c, m, [40, 3], "bf16", 73)
+    refused(c, m, "bf16", n.TQ_ERR_INVALID_ARG, lambda: c.extend(i32([1, 2]), i32([0, 5, 9]), total=8))
+    with pytest.raises(n.TQError):
+        c.extend(i32([1]), i32([0, 5]), total=-1)
+    same_tables(c, m)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("code,d,page", [("int8", 128, 32), ("e4m3", 64, 128), ("int8", 256, 64)])
+@pytest.mark.parametrize("counts", [(5, 1), (200, 40), (0, 300)])
+def test_a_write_that_is_given_too_few_tokens_stores_zeros(dtype, code, d, page, counts):
+    """Nothing of what the pages or tails held before shows, and later appends build on the zeros."""
+    from compressed_attention_turboquantprod_b200 import TQError
+    c, m = make(2, d, 40, 3, 12, page, code, dtype)
+    dirty(c, m, dtype)
+    fill(c, m, [page // 2 + 3, 1], dtype, 75)
+    total = sum(counts)
+    c.extend(i32([0, 2]), offsets(counts))
+    short = tokens(total - 1 if total < 100 else 2, 2, d, dtype, 76)
+    c.write(short, short)
+    with pytest.raises(TQError) as e:
+        c.check()
+    assert e.value.status == nat().TQ_ERR_INVALID_ARG
+    for s, n in zip((0, 2), counts):
+        m.append(s, [(np.zeros((n, 2, d)),) * 2])
+    same_tables(c, m)
+    same_values(c, m, dtype)
+    fill(c, m, [3, page, 2], dtype, 77)
+    same_tables(c, m)
+    same_values(c, m, dtype)
+
+
+def test_a_captured_write_behind_another_plan():
+    """A graph holds a write for one row; a plan of nine rows comes before its replay."""
+    from compressed_attention_turboquantprod_b200 import TQError
+    c, m = make(1, 64, 40, 10, 4, 16, "int8", "f16")
+    dirty(c, m, "f16")
+    K = tokens(400, 1, 64, "f16", 78)
+    c.extend(i32([0]), i32([0, 1]))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.write(K, K)
+    g.replay()
+    m.append(0, [(host(K[:1]),) * 2])
+    c.check()
+    c.extend(i32(range(1, 10)), offsets([30] * 9))
+    g.replay()
+    with pytest.raises(TQError):
+        c.check()
+    for s in range(1, 10):
+        m.append(s, [(np.zeros((30, 1, 64)),) * 2])
+    same_tables(c, m)
+    same_values(c, m, "f16")
