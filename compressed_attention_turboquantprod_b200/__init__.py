@@ -322,7 +322,7 @@ class PagedKVCache:
             raise ValueError("out must have Q's shape and dtype")
         if lse is not None and (lse.shape != (tokens, Hq) or lse.dtype != torch.float32):
             raise ValueError("lse must be float32 [tokens, Hq]")
-        with self._on(Q, slots, cu, out, lse):
+        with self._on(Q, slots, cu, out, lse, workspace):
             ws = self.workspace() if workspace is None else workspace
             native.tq_paged_attention(self.state, layer, Q, slots, cu, max_q, causal, scale, out,
                                       lse, ws)
