@@ -1,5 +1,6 @@
 """PagedKVCache's own checks, without a GPU: tensors that say they are on the cache's device, and a
 library whose calls are only recorded."""
+import importlib
 import types
 
 import pytest
@@ -19,7 +20,8 @@ def on(t):
 def cache(monkeypatch):
     from compressed_attention_turboquantprod_b200 import build
     build.build()
-    from compressed_attention_turboquantprod_b200 import PagedKVCache, native
+    from compressed_attention_turboquantprod_b200 import PagedKVCache
+    native = importlib.import_module("compressed_attention_turboquantprod_b200.native")
     c = PagedKVCache.__new__(PagedKVCache)
     c.desc = native.make_paged_desc(1, 2, 64, 16, 10, 4, 5, torch.bfloat16, 0)
     c.dtype, c._index, c._ws, c._cu = torch.bfloat16, 0, {}, {}
@@ -27,8 +29,8 @@ def cache(monkeypatch):
     c.state = native.tq_paged_layout(c.desc)
     c.calls = []
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    for name in dir(native):
-        if name.startswith("tq_paged_") and name not in ("tq_paged_desc",):
+    for name, f in list(vars(native).items()):
+        if name.startswith("tq_paged_") and isinstance(f, types.FunctionType):
             monkeypatch.setattr(native, name, lambda *a, _n=name, **k: c.calls.append(_n))
     return c
 
