@@ -294,8 +294,7 @@ class PagedKVCache:
             raise ValueError("a cache of several layers takes extend() and a write() per layer")
         self._typed(K, V)
         with self._on(K, V, slots, cu):
-            native.tq_paged_extend_within(self.state, slots, cu, K.shape[0])
-            native.tq_paged_write(self.state, 0, K, V)
+            native.tq_paged_append(self.state, slots, cu, K, V)
 
     def read(self, slots: torch.Tensor, cu: torch.Tensor, total: int, layer: int = 0):
         """The first cu[i+1]-cu[i] tokens of each slot as floats: (K, V), [total, Hkv, d]."""
@@ -306,6 +305,18 @@ class PagedKVCache:
         return K, V
 
     # ---- attention
+    def _queries(self, Q, slots, cu, out=None, lse=None, workspace=None):
+        """What can be checked of an attention call without the library; (the device made current,
+        what native.check_queries gives)."""
+        queries = native.check_queries(self.state, Q, slots, cu)
+        if Q.dtype != self.dtype:
+            raise ValueError(f"expected {self.dtype}, got {Q.dtype}")
+        if out is not None and (out.shape != Q.shape or out.dtype != self.dtype):
+            raise ValueError("out must have Q's shape and dtype")
+        if lse is not None and (lse.shape != Q.shape[:2] or lse.dtype != torch.float32):
+            raise ValueError("lse must be float32 [tokens, Hq]")
+        return self._on(Q, slots, cu, out, lse, workspace), queries
+
     def attend(self, Q: torch.Tensor, slots: torch.Tensor, cu: torch.Tensor, max_q: int,
                causal: bool = True, softmax_scale: Optional[float] = None, layer: int = 0,
                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
@@ -313,19 +324,18 @@ class PagedKVCache:
         """Row i's queries Q[cu[i]:cu[i+1]] over the tokens of slots[i].  causal: they are the
         sequence's last tokens, each sees the tokens up to itself.  out and lse (float32
         [tokens, Hq], log-sum-exp of the scaled logits) may be given."""
-        tokens, Hq, d = Q.shape
-        self._typed(Q)
-        scale = 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale
+        on, queries = self._queries(Q, slots, cu, out, lse, workspace)
+        with on:
+            return self._attend(queries, Q, slots, cu, max_q, causal, softmax_scale, layer, out, lse,
+                                workspace)
+
+    def _attend(self, queries, Q, slots, cu, max_q, causal, softmax_scale, layer, out, lse, workspace):
+        scale = 1.0 / math.sqrt(self.desc.d) if softmax_scale is None else softmax_scale
         if out is None:
-            out = torch.empty(tokens, Hq, d, dtype=self.dtype, device=Q.device)
-        elif out.shape != Q.shape or out.dtype != self.dtype:
-            raise ValueError("out must have Q's shape and dtype")
-        if lse is not None and (lse.shape != (tokens, Hq) or lse.dtype != torch.float32):
-            raise ValueError("lse must be float32 [tokens, Hq]")
-        with self._on(Q, slots, cu, out, lse, workspace):
-            ws = self.workspace() if workspace is None else workspace
-            native.tq_paged_attention(self.state, layer, Q, slots, cu, max_q, causal, scale, out,
-                                      lse, ws)
+            out = torch.empty(Q.shape, dtype=self.dtype, device=Q.device)
+        ws = self.workspace() if workspace is None else workspace
+        native.tq_paged_attention(self.state, layer, Q, slots, cu, max_q, causal, scale, out, lse, ws,
+                                  queries=queries)
         return out
 
     def _ones(self, n: int) -> torch.Tensor:
@@ -344,11 +354,17 @@ class PagedKVCache:
         return self.attend(Q, slots, cu, 1, True, softmax_scale, layer, **kw)
 
     def decode_step(self, K: torch.Tensor, V: torch.Tensor, Q: torch.Tensor, slots: torch.Tensor,
-                    cu: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None, **kw):
-        """append() one token per slot (K, V [n, Hkv, d]), then decode()."""
+                    cu: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None,
+                    layer: int = 0, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+        """append() one token per slot (K, V [n, Hkv, d]), then decode().  What can be said of Q
+        without the library is checked before the append."""
         cu = self._ones(slots.numel()) if cu is None else cu
-        self.append(K, V, slots, cu)
-        return self.decode(Q, slots, softmax_scale, cu=cu, **kw)
+        on, queries = self._queries(Q, slots, cu, out, lse, workspace)
+        with on:
+            self.append(K, V, slots, cu)
+            return self._attend(queries, Q, slots, cu, 1, True, softmax_scale, layer, out, lse,
+                                workspace)
 
     def cross(self, Q: torch.Tensor, slots: torch.Tensor, cu: torch.Tensor, max_q: int,
               softmax_scale: Optional[float] = None, layer: int = 0, **kw):

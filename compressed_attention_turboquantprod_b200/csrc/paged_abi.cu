@@ -149,6 +149,18 @@ bool bad_stride(const tq_paged* c, int64_t stride, int64_t heads) {
   return stride < heads * c->desc.d || stride * tq::paged_esize(c->desc.dtype) % 16 != 0;
 }
 
+int check_tokens(const tq_paged* c, const void* K, const void* V, int64_t k_stride, int64_t v_stride, int64_t total,
+                 const char* name) {
+  if (total < 0 || total > INT_MAX) return set_error(TQ_ERR_INVALID_ARG, "%s: total=%lld", name, (long long)total);
+  if (total == 0) return TQ_OK;
+  if (!K || !V || !aligned(K, 16) || !aligned(V, 16))
+    return set_error(TQ_ERR_INVALID_ARG, "%s: K and V must be non-null, 16-byte aligned", name);
+  if (bad_stride(c, k_stride, c->desc.Hkv) || bad_stride(c, v_stride, c->desc.Hkv))
+    return set_error(TQ_ERR_INVALID_ARG, "%s: token strides %lld, %lld: at least Hkv * d, multiples of 16 bytes", name,
+                     (long long)k_stride, (long long)v_stride);
+  return TQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -201,19 +213,28 @@ int tq_paged_write(const tq_paged* c, int layer, const void* K, const void* V, i
   TQ_FAULT_POINT("tq_paged_write");
   int st = check_layer(c, layer, "tq_paged_write");
   if (st != TQ_OK) return st;
-  if (total < 0 || total > INT_MAX) return set_error(TQ_ERR_INVALID_ARG, "tq_paged_write: total=%lld", (long long)total);
+  st = check_tokens(c, K, V, k_stride, v_stride, total, "tq_paged_write");
+  if (st != TQ_OK) return st;
   if (total == 0) return tq::clear_error();
-  if (!K || !V || !aligned(K, 16) || !aligned(V, 16))
-    return set_error(TQ_ERR_INVALID_ARG, "tq_paged_write: K and V must be non-null, 16-byte aligned");
-  if (bad_stride(c, k_stride, c->desc.Hkv) || bad_stride(c, v_stride, c->desc.Hkv))
-    return set_error(TQ_ERR_INVALID_ARG, "tq_paged_write: token strides %lld, %lld: at least Hkv * d, multiples of 16 bytes",
-                     (long long)k_stride, (long long)v_stride);
   if (c->plan_rows < 1) return set_error(TQ_ERR_INVALID_ARG, "tq_paged_write: no tq_paged_extend before it");
   st = check_pending("tq_paged_write");
   if (st != TQ_OK) return st;
   return done(tq::paged_launch_write(geom(c), layer, K, V, k_stride, v_stride, total, c->plan_rows,
                                      static_cast<cudaStream_t>(stream)),
               "tq_paged_write");
+}
+
+int tq_paged_append(tq_paged* c, const int32_t* slots, const int32_t* cu, int n, const void* K, const void* V,
+                    int64_t k_stride, int64_t v_stride, int64_t total, void* stream) {
+  TQ_FAULT_POINT("tq_paged_append");
+  int st = check_layer(c, 0, "tq_paged_append");
+  if (st == TQ_OK && c->desc.layers != 1)
+    st = set_error(TQ_ERR_INVALID_ARG, "tq_paged_append: layers=%d, not 1", c->desc.layers);
+  if (st == TQ_OK) st = check_tokens(c, K, V, k_stride, v_stride, total, "tq_paged_append");
+  if (st == TQ_OK) st = extend(c, slots, cu, n, total, stream, "tq_paged_append");
+  if (st != TQ_OK || total == 0) return st;
+  return done(tq::paged_launch_write(geom(c), 0, K, V, k_stride, v_stride, total, n, static_cast<cudaStream_t>(stream)),
+              "tq_paged_append");
 }
 
 int tq_paged_read(const tq_paged* c, int layer, const int32_t* slots, const int32_t* cu, int n, int64_t total, void* K,

@@ -122,6 +122,7 @@ def _load() -> ctypes.CDLL:
         "tq_paged_extend": (I, [G, P, P, I, P]),
         "tq_paged_extend_within": (I, [G, P, P, I, I64, P]),
         "tq_paged_write": (I, [G, I, P, P, I64, I64, I64, P]),
+        "tq_paged_append": (I, [G, P, P, I, P, P, I64, I64, I64, P]),
         "tq_paged_read": (I, [G, I, P, P, I, I64, P, P, P]),
         "tq_paged_table": (I, [G, P, I, P, P]),
         "tq_paged_workspace_bytes": (SZ, [G]),
@@ -427,11 +428,21 @@ def tq_paged_extend_within(cache: tq_paged, slots, cu, total: int, stream=None):
                                       total, _stream_fast(stream)), "tq_paged_extend_within")
 
 
-def tq_paged_write(cache: tq_paged, layer: int, K, V, stream=None):
+def _key_values(cache: tq_paged, K, V):
     if K.shape[0] != V.shape[0]:
         raise ValueError("K and V have different token counts")
     (kp, ks), (vp, vs) = (_tokens(t, cache.desc.Hkv, cache.desc.d) for t in (K, V))
-    _check(lib.tq_paged_write(ctypes.byref(cache), layer, kp, vp, ks, vs, K.shape[0],
+    return kp, vp, ks, vs, K.shape[0]
+
+
+def tq_paged_append(cache: tq_paged, slots, cu, K, V, stream=None):
+    _check(lib.tq_paged_append(ctypes.byref(cache), _i32(slots), _i32(cu), _rows(slots, cu),
+                               *_key_values(cache, K, V), _stream_fast(stream)), "tq_paged_append")
+
+
+def tq_paged_write(cache: tq_paged, layer: int, K, V, stream=None):
+    kp, vp, ks, vs, total = _key_values(cache, K, V)
+    _check(lib.tq_paged_write(ctypes.byref(cache), layer, kp, vp, ks, vs, total,
                               _stream_fast(stream)), "tq_paged_write")
 
 
@@ -454,13 +465,25 @@ def tq_paged_workspace_init(cache: tq_paged, workspace, stream=None):
                                        _stream_fast(stream)), "tq_paged_workspace_init")
 
 
+def check_queries(cache: tq_paged, Q, slots, cu):
+    """(tokens, heads, address, token stride, rows) of a call's queries, which come as for _tokens."""
+    shape, want = Q.shape, cache.desc.d
+    if len(shape) != 3 or shape[2] != want:
+        raise ValueError(f"expected queries [tokens, heads, {want}], got {tuple(shape)}")
+    tokens, heads, d = shape
+    stride, by_head, by_entry = Q.stride()
+    if by_entry != 1 or (heads > 1 and by_head != d):
+        raise ValueError("the heads of a token must be contiguous")
+    return tokens, heads, Q.data_ptr(), stride if tokens > 1 else heads * d, _rows(slots, cu)
+
+
 def tq_paged_attention(cache: tq_paged, layer: int, Q, slots, cu, max_q: int, causal: bool,
-                       softmax_scale: float, out, lse, workspace, stream=None):
-    """Q [total_q, Hq, d] (token views as for K and V); out contiguous; lse or None."""
-    Hq = Q.shape[1]
-    qp, qs = _tokens(Q, Hq, cache.desc.d)
+                       softmax_scale: float, out, lse, workspace, stream=None, queries=None):
+    """Q [total_q, Hq, d] (token views as for K and V); out contiguous; lse or None.
+    queries: what check_queries gave for Q."""
+    tokens, Hq, qp, qs, rows = queries or check_queries(cache, Q, slots, cu)
     _check(lib.tq_paged_attention(ctypes.byref(cache), layer, qp, qs, Hq, _i32(slots), _i32(cu),
-                                  _rows(slots, cu), max_q, Q.shape[0], int(causal), softmax_scale,
+                                  rows, max_q, tokens, int(causal), softmax_scale,
                                   _addr(out), _addr(lse), _addr(workspace), _ws(workspace),
                                   _stream_fast(stream)), "tq_paged_attention")
 

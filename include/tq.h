@@ -582,6 +582,13 @@ int tq_paged_write(const tq_paged* c, int layer, const void* K, const void* V, i
                    int64_t v_stride, int64_t total, void* stream);
 
 /*
+ * tq_paged_append -- tq_paged_extend_within and tq_paged_write of a cache of one layer, with
+ * every host check of both before either is launched.  Errors: INVALID_ARG, CUDA.
+ */
+int tq_paged_append(tq_paged* c, const int32_t* slots, const int32_t* cu, int n, const void* K,
+                    const void* V, int64_t k_stride, int64_t v_stride, int64_t total, void* stream);
+
+/*
  * tq_paged_read -- the first cu[i+1] - cu[i] cached tokens of slot slots[i] as
  * floats (code * scale rounded once to desc.dtype; zeros past the sequence's end)
  * into K, V [total][Hkv][d] at tokens cu[i].. .  Rows outside [cu[0], cu[n]) are

@@ -1,5 +1,6 @@
 """PagedKVCache's own checks, without a GPU: tensors that say they are on the cache's device, and a
 library whose calls are only recorded."""
+import ctypes
 import importlib
 import types
 
@@ -16,6 +17,19 @@ def on(t):
     return t.as_subclass(OnDevice)
 
 
+class Library:
+    """Every call succeeds and is noted."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return 0
+        return call
+
+
 @pytest.fixture
 def cache(monkeypatch):
     from compressed_attention_turboquantprod_b200 import build
@@ -27,11 +41,11 @@ def cache(monkeypatch):
     c.dtype, c._index, c._ws, c._cu = torch.bfloat16, 0, {}, {}
     c.buffer = types.SimpleNamespace(device=torch.device("cuda", 0))
     c.state = native.tq_paged_layout(c.desc)
-    c.calls = []
+    lib = Library()
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    for name, f in list(vars(native).items()):
-        if name.startswith("tq_paged_") and isinstance(f, types.FunctionType):
-            monkeypatch.setattr(native, name, lambda *a, _n=name, **k: c.calls.append(_n))
+    monkeypatch.setattr(native, "raw_stream", lambda device: 0)
+    monkeypatch.setattr(native, "lib", lib)
+    c.calls = lib.calls
     return c
 
 
@@ -47,3 +61,55 @@ def test_a_workspace_of_another_device_is_refused(cache):
     assert cache.calls == []
     cache.attend(*args, out=out, workspace=on(torch.zeros(1 << 20, dtype=torch.uint8)))
     assert cache.calls == ["tq_paged_attention"]
+
+
+def test_an_append_is_checked_before_its_plan(cache):
+    bf, z = torch.bfloat16, torch.zeros
+    good, slots, cu = on(z(3, 2, 64, dtype=bf)), i32([0]), i32([0, 3])
+    for K, V, s, o in ((good, good[:2], slots, cu), (on(z(3, 2, 32, dtype=bf)),) * 2 + (slots, cu),
+                       (good, on(z(3, 64, 2, dtype=bf)).transpose(1, 2), slots, cu), (good, good, slots, i32([0])),
+                       (good, good, slots, on(torch.tensor([0, 3]))), (good, on(z(3, 2, 64)), slots, cu),
+                       (good, z(3, 2, 64, dtype=bf), slots, cu)):
+        with pytest.raises(ValueError):
+            cache.append(K, V, s, o)
+        assert cache.calls == []
+    cache.append(good, good, slots, cu)
+    assert cache.calls == ["tq_paged_append"]
+
+
+def test_a_decode_step_is_checked_before_its_append(cache):
+    bf, z = torch.bfloat16, torch.zeros
+    K, slots, cu, ws = on(z(1, 2, 64, dtype=bf)), i32([0]), i32([0, 1]), on(z(64, dtype=torch.uint8))
+    Q, out = (on(z(1, 4, 64, dtype=bf)) for _ in range(2))
+    for q, kw in ((on(z(1, 4, 32, dtype=bf)), {}), (on(z(1, 4, 64)), {}), (on(z(4, 64, dtype=bf)), {}),
+                  (z(1, 4, 64, dtype=bf), {}), (Q, dict(out=on(z(1, 4, 64)))), (Q, dict(lse=on(z(1, 3)))),
+                  (Q, dict(workspace=z(64)))):
+        with pytest.raises(ValueError):
+            cache.decode_step(K, K, q, slots, cu, **{**dict(out=out, workspace=ws), **kw})
+        assert cache.calls == []
+    cache.decode_step(K, K, Q, slots, cu, out=out, workspace=ws)
+    assert cache.calls == ["tq_paged_append", "tq_paged_attention"]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="uses fake device pointers")
+def test_append_refusals_of_the_library():
+    native = importlib.import_module("compressed_attention_turboquantprod_b200.native")
+    L, bad, S = native.lib, native.TQ_ERR_INVALID_ARG, None
+    fake, odd, w = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 4), 2 * 64
+    c = native.tq_paged_layout(native.make_paged_desc(1, 2, 64, 16, 10, 4, 5, torch.bfloat16, 0))
+    c.base = 1 << 20
+
+    def append(c=c, slots=fake, cu=fake, n=1, K=fake, V=fake, ks=w, vs=w, total=5):
+        return L.tq_paged_append(ctypes.byref(c), slots, cu, n, K, V, ks, vs, total, S)
+    for kw in (dict(slots=None), dict(cu=ctypes.c_void_p(3)), dict(n=0), dict(n=5), dict(K=None), dict(V=odd), dict(ks=w - 8),
+               dict(vs=w + 4), dict(total=-1), dict(total=1 << 31)):
+        assert append(**kw) == bad, kw
+        assert c.plan_rows == 0
+    two = native.tq_paged_layout(native.make_paged_desc(2, 2, 64, 16, 10, 4, 5, torch.bfloat16, 0))
+    two.base = 1 << 20
+    assert append(c=two) == bad
+    assert L.tq_paged_extend_within(ctypes.byref(c), fake, fake, 1, -1, S) == bad
+    for name, args in (("tq_paged_append", (fake, fake, 1, fake, fake, w, w, 5, S)), ("tq_paged_extend_within", (fake, fake, 1, 5, S))):
+        native.tq_debug_fail_next(name)
+        assert getattr(L, name)(ctypes.byref(c), *args) == native.TQ_ERR_CUDA
+        assert L.tq_last_error() == b"injected fault"
