@@ -167,6 +167,7 @@ __device__ __noinline__ void write_zeros(const PGeom& g, int layer, int h, int k
     const int n0 = max(row.start, t0) - t0, n1 = min(end, t0 + g.page) - t0;
     if (n1 <= n0) continue;
     const int pid = g.table[(int64_t)row.slot * g.max_pages + p];
+    if (g.len[row.slot] != end) continue;                              // (freed since: its pages are not its own)
     if ((unsigned)pid >= (unsigned)g.pages) {
       if (threadIdx.x == 0) atomicOr(&g.state->status, kPagedBadPage);
       continue;
@@ -230,6 +231,10 @@ __global__ void __launch_bounds__(kWThreads) k_paged_write(const __grid_constant
   const int n0 = max(row.start, t0) - t0, n1 = min(row.start + row.count, t0 + g.page) - t0;
   if (n1 <= n0) return;
   const int pid = g.table[(int64_t)row.slot * g.max_pages + p];
+  if (g.len[row.slot] != row.start + row.count) {   // freed since the plan: its pages may be another sequence's
+    if (tid == 0) atomicOr(&g.state->status, kPagedBadSlot);
+    return;
+  }
   if ((unsigned)pid >= (unsigned)g.pages) {
     if (tid == 0) atomicOr(&g.state->status, kPagedBadPage);
     return;

@@ -552,7 +552,8 @@ int tq_paged_init(tq_paged* c, const tq_paged_desc* desc, void* dev_mem, size_t 
  * tq_paged_extend -- take pages for new tokens: row i (0 <= i < n) appends
  * cu[i+1] - cu[i] tokens to slot slots[i]; slot -1 is a padding row whose tokens
  * are left out.  The new tokens become visible at once: write every layer
- * (tq_paged_write) before attending and before the next tq_paged_extend.
+ * (tq_paged_write) before attending, before the next tq_paged_extend and before the
+ * slot is forked, copied or freed.
  *   slots  device int32[n], no slot twice;  cu  device int32[n+1], cu[0] >= 0, not
  *          decreasing
  *   n      1..desc.slots
@@ -572,7 +573,8 @@ int tq_paged_init(tq_paged* c, const tq_paged_desc* desc, void* dev_mem, size_t 
  *   total    tokens in K and V (0: nothing to do)
  * Device checks: INVALID_ARG (the last plan reaches past `total`, or has more rows than
  * the one that was last extended from the host when this call was made or captured: all
- * of the plan's tokens are then stored as zeros).
+ * of the plan's tokens are then stored as zeros; a slot that was freed since the plan:
+ * its row is left out).
  * Errors: INVALID_ARG, CUDA.
  */
 int tq_paged_extend(tq_paged* c, const int32_t* slots, const int32_t* cu, int n, void* stream);

@@ -107,3 +107,23 @@ def test_a_captured_write_behind_another_plan():
         m.append(s, [(np.zeros((30, 1, 64)),) * 2])
     same_tables(c, m)
     same_values(c, m, "f16")
+
+
+def test_a_slot_freed_before_its_write_is_left_out():
+    """Its page has gone to another sequence's fork by then."""
+    from compressed_attention_turboquantprod_b200 import TQError
+    c, m = make(2, 64, 12, 4, 4, 16, "int8", "f16")
+    fill(c, m, [1], "f16", 81, slots=[2])
+    K = tokens(30, 2, 64, "f16", 82)
+    c.extend(i32([0, 1]), i32([0, 20, 30]))
+    c.free(i32([0]))
+    c.fork(i32([2]), i32([3]))
+    c.write(K, K)
+    with pytest.raises(TQError) as e:
+        c.check()
+    assert e.value.status == nat().TQ_ERR_INVALID_ARG
+    table = c.page_table(i32([1, 3])).cpu()
+    assert table[1, 0] == 1 and table[0, 0] == 3          # pages 1 and 2 were slot 0's
+    m.append(1, [(host(K[20:]),) * 2])
+    m.fork(2, 3)
+    same_values(c, m, "f16")
