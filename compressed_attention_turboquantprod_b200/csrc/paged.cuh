@@ -117,6 +117,7 @@ cudaError_t paged_launch_free(const PGeom& g, const int* slots, int n, cudaStrea
 cudaError_t paged_launch_branch(const PGeom& src, const PGeom& dst, const int* from, const int* to, int n,
                                 bool share, cudaStream_t s);
 cudaError_t paged_launch_compact(const PGeom& g, cudaStream_t s);
+cudaError_t paged_launch_clear(const PGeom& g, int bits, cudaStream_t s);      // of the status
 cudaError_t paged_launch_table(const PGeom& g, const int* slots, int n, int* out, cudaStream_t s);
 
 struct PagedAttn {

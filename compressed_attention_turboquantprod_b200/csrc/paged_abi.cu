@@ -2,6 +2,7 @@
 // before any launch.
 #include <climits>
 #include <cmath>
+#include <cstdio>
 #include <cstring>
 
 #include "paged.cuh"
@@ -379,18 +380,32 @@ int tq_paged_check(tq_paged* c, int32_t* free_pages, void* stream) {
   static_assert(offsetof(tq::PagedState, status) == 0 && offsetof(tq::PagedState, n_free) == 4, "read together");
   cudaError_t e = cudaMemcpyAsync(v, g.state, sizeof(v), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && v[0] != 0) e = cudaMemsetAsync(g.state, 0, 4, s);
+  // (only what is reported: a call on another stream may fail meanwhile)
+  if (e == cudaSuccess && v[0] != 0) e = tq::paged_launch_clear(g, v[0], s);
   if (e != cudaSuccess) return cuda_fail(e, "tq_paged_check");
   if (free_pages) *free_pages = v[1];
-  if (v[0] & tq::kPagedWait) return set_error(TQ_ERR_CUDA, "a paged attention's bounded wait gave up");
-  if (v[0] & tq::kPagedNoPages) return set_error(TQ_ERR_CAPACITY, "not enough free pages (%d free)", v[1]);
-  if (v[0] & tq::kPagedTooLong) return set_error(TQ_ERR_CAPACITY, "a sequence would outgrow max_pages=%d", c->desc.max_pages);
-  if (v[0] & tq::kPagedBadSlot) return set_error(TQ_ERR_INVALID_ARG, "a slot out of range or named twice");
-  if (v[0] & tq::kPagedBadOffsets) return set_error(TQ_ERR_INVALID_ARG, "token offsets that decrease, leave the arrays or pass max_q");
-  if (v[0] & tq::kPagedNotEmpty) return set_error(TQ_ERR_INVALID_ARG, "a fork or copy into a slot that is not empty");
-  if (v[0] & tq::kPagedBadWorkspace) return set_error(TQ_ERR_INVALID_ARG, "an attention workspace that was not initialised");
-  if (v[0] != 0) return set_error(TQ_ERR_INVALID_ARG, "a page table entry out of range");
-  return tq::clear_error();
+  if (v[0] == 0) return tq::clear_error();
+  const struct {
+    int bit, status;
+    const char* what;
+  } reasons[] = {{tq::kPagedWait, TQ_ERR_CUDA, "a paged attention's bounded wait gave up"},
+                 {tq::kPagedNoPages, TQ_ERR_CAPACITY, "not enough free pages"},
+                 {tq::kPagedTooLong, TQ_ERR_CAPACITY, "a sequence would outgrow max_pages"},
+                 {tq::kPagedBadSlot, TQ_ERR_INVALID_ARG, "a slot out of range, named twice, or freed before its write"},
+                 {tq::kPagedBadOffsets, TQ_ERR_INVALID_ARG, "token offsets that decrease, leave the arrays or pass max_q"},
+                 {tq::kPagedNotEmpty, TQ_ERR_INVALID_ARG, "a fork or copy into a slot that is not empty"},
+                 {tq::kPagedBadWorkspace, TQ_ERR_INVALID_ARG, "an attention workspace that was not initialised"},
+                 {tq::kPagedBadPage, TQ_ERR_INVALID_ARG, "a page table entry out of range"}};
+  char text[512] = "";
+  int status = TQ_OK;
+  for (const auto& r : reasons)
+    if (v[0] & r.bit) {
+      if (status == TQ_OK) status = r.status;
+      const size_t at = std::strlen(text);
+      std::snprintf(text + at, sizeof(text) - at, "%s%s", at ? "; " : "", r.what);
+    }
+  return set_error(status == TQ_OK ? TQ_ERR_CUDA : status, "%s (%d pages free, max_pages=%d)", text, v[1],
+                   c->desc.max_pages);
 }
 
 }  // extern "C"

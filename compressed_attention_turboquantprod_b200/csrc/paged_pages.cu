@@ -432,6 +432,11 @@ __global__ void __launch_bounds__(kMoveThreads) k_paged_move(PGeom src, PGeom ds
   }
 }
 
+__global__ void k_paged_clear(PGeom g, int bits) {
+  pdl_wait();
+  atomicAnd(&g.state->status, ~bits);
+}
+
 // Rows of the page table, -1 where a sequence has no page.
 __global__ void __launch_bounds__(kMoveThreads) k_paged_table(PGeom g, const int* slots, int n, int* out) {
   pdl_wait();
@@ -472,6 +477,10 @@ cudaError_t paged_launch_compact(const PGeom& g, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   return launch_pdl(k_paged_move, dim3(148 * 4), dim3(kMoveThreads), 0, s, g, g, (const int*)nullptr,
                     (const int*)nullptr, 0);
+}
+
+cudaError_t paged_launch_clear(const PGeom& g, int bits, cudaStream_t s) {
+  return launch_pdl(k_paged_clear, dim3(1), dim3(1), 0, s, g, bits);
 }
 
 cudaError_t paged_launch_table(const PGeom& g, const int* slots, int n, int* out, cudaStream_t s) {

@@ -660,7 +660,8 @@ int tq_paged_compact(tq_paged* c, void* stream);
 /*
  * tq_paged_check -- SYNCHRONOUS: waits for `stream`, then reports (and clears) the
  * sticky status of the cache: CAPACITY, INVALID_ARG or CUDA (a bounded wait gave
- * up) with the reason in tq_last_error(); free_pages (may be NULL) receives the
+ * up), the first of these that there is, with every reason in tq_last_error(); what
+ * calls on other streams report meanwhile stays for the next check.  free_pages (may be NULL) receives the
  * number of free pages.
  */
 int tq_paged_check(tq_paged* c, int32_t* free_pages, void* stream);

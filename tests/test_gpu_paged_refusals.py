@@ -127,3 +127,21 @@ def test_a_slot_freed_before_its_write_is_left_out():
     m.append(1, [(host(K[20:]),) * 2])
     m.fork(2, 3)
     same_values(c, m, "f16")
+
+
+def test_check_reports_every_reason_once():
+    from compressed_attention_turboquantprod_b200 import TQError
+    n = nat()
+    c, m = make(1, 64, 6, 4, 4, 16, "int8", "f16")
+    fill(c, m, [20], "f16", 91)
+    K = tokens(80, 1, 64, "f16", 92)
+    c.append(K, K, i32([2, 2]), i32([0, 1, 2]))            # a slot twice
+    c.append(K, K, i32([1, 2]), i32([0, 40, 80]))          # six pages, four are free
+    c.fork(i32([1]), i32([0]))                             # not empty
+    with pytest.raises(TQError) as e:
+        c.check()
+    assert e.value.status == n.TQ_ERR_CAPACITY
+    for text in ("free pages", "named twice", "not empty"):
+        assert text in e.value.message
+    assert c.check() == 4
+    same_tables(c, m)
