@@ -277,6 +277,12 @@ int tq_debug_bounds_check(void) {
   return ok();
 }
 
+int tq_debug_paged_lose_copies(int on) {
+  const cudaError_t e = tq::paged_lose_copies(on);
+  if (e == cudaErrorNotSupported) return fail(TQ_ERR_UNSUPPORTED, "only in the bounds-checked build");
+  return e == cudaSuccess ? ok() : cuda_fail(e, "tq_debug_paged_lose_copies");
+}
+
 int tq_version(void) { return 1; }
 
 int tq_debug_fail_next(const char* name) {

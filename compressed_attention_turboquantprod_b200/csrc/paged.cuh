@@ -138,6 +138,7 @@ size_t paged_attn_ws_bytes(int d);
 // many query rows (paged_chunk.cu)
 size_t paged_chunk_ws_bytes(int d);
 cudaError_t paged_launch_chunk(const PGeom& g, const PagedAttn& a, cudaStream_t s);
+cudaError_t paged_lose_copies(int on);                                          // see tq_debug_paged_lose_copies
 cudaError_t paged_launch_ws_init(void* ws, cudaStream_t s);
 cudaError_t paged_launch_attention(const PGeom& g, const PagedAttn& a, cudaStream_t s);
 

@@ -7,6 +7,15 @@ namespace tq {
 namespace {
 using namespace paged;
 
+// In the bounds-checked build tq_debug_paged_lose_copies makes the decode's copies fail their check, so
+// that its waits run out, after a short time then.
+#ifdef TQ_DEBUG_BOUNDS
+__device__ int g_lose_copies;
+#define TQ_LOSE_COPIES (*static_cast<volatile int*>(&g_lose_copies) != 0)
+#else
+#define TQ_LOSE_COPIES false
+#endif
+
 __global__ void k_paged_ws_init(uint32_t* ws) {
   pdl_wait();
   for (int i = threadIdx.x; i < (int)(kWsHeader / 4); i += blockDim.x) ws[i] = i == 0 ? kWsMagic : 0u;
@@ -174,9 +183,10 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
         pid = 0;
       }
       const int tk = min((int)(xi - nxt.u0) * kTile + lane * SUB, nxt.s.len - 1);
-      cache_bulk_load(ring + ist * STB + lane * SS,
-                      paged_block(g, a.layer, pid, kv, nxt.h, (tk & (g.page - 1)) / SUB), SUB * D + kPagedTrailer, bar,
-                      g.base, g.total, 401);
+      if (!TQ_LOSE_COPIES)
+        cache_bulk_load(ring + ist * STB + lane * SS,
+                        paged_block(g, a.layer, pid, kv, nxt.h, (tk & (g.page - 1)) / SUB), SUB * D + kPagedTrailer, bar,
+                        g.base, g.total, 401);
     }
     ist = ist + 1 == NST ? 0 : ist + 1;
   };
@@ -192,8 +202,18 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
   };
   int cst = 0;
   uint32_t cph = 0;
+  bool lost = false;
+  int uvis = 0;                             // tokens that the unit's last row sees
   auto wait_stage = [&]() {
-    if (!mbar_wait_timed(&s_full[warp][cst], cph, &s_abort)) atomicOr(&g.state->status, kPagedWait);
+    const bool ok = mbar_wait_timed(&s_full[warp][cst], cph, &s_abort, TQ_LOSE_COPIES ? 1ll << 26 : kWaitCycles);
+    // A wait that gave up ends the warp's requests (a stage still in flight must not be asked for again)
+    // and its tiles: the call runs out on what there is, and the status says so.
+    if (!__all_sync(0xffffffffu, ok)) {
+      atomicOr(&g.state->status, kPagedWait);
+      lost = true;
+      xi = x1;
+      uvis = 0;
+    }
   };
   auto next_stage = [&]() {
     if (++cst == NST) {
@@ -283,7 +303,7 @@ __global__ void __launch_bounds__(kDecThreads, DecCfg<D>::kCtas) k_paged_decode(
     __syncthreads();
     const float fr = s_fr[gi];
     const int vis = s_vis[gi];
-    const int uvis = group_visible<kDecRows>(cur.s, G, cur.rg, a.causal);
+    uvis = lost ? 0 : group_visible<kDecRows>(cur.s, G, cur.rg, a.causal);
     float m = -INFINITY, l = 0.f;
     float o[NT][2];
 #pragma unroll
@@ -570,6 +590,13 @@ cudaError_t decode_d(const PGeom& g, const PagedAttn& a, cudaStream_t s) {
 size_t paged_attn_ws_bytes(int d) {
   const size_t decode = kWsHeader + (size_t)2 * kMaxCtas * kDecRows * (8 + 4 * (size_t)d), chunk = paged_chunk_ws_bytes(d);
   return decode > chunk ? decode : chunk;
+}
+cudaError_t paged_lose_copies(int on) {
+#ifdef TQ_DEBUG_BOUNDS
+  return cudaMemcpyToSymbol(g_lose_copies, &on, sizeof(on));
+#else
+  return cudaErrorNotSupported;
+#endif
 }
 cudaError_t paged_launch_ws_init(void* ws, cudaStream_t s) {
   return launch_pdl(k_paged_ws_init, dim3(1), dim3(256), 0, s, static_cast<uint32_t*>(ws));

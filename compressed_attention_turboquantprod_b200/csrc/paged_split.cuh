@@ -287,13 +287,14 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Wait on phase `parity` for at most 2^31 cycles (about a second); once a wait of the CTA has given
-// up (*abort), none waits any more.
-__device__ __forceinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, int* abort) {
+// Wait on phase `parity` for at most `cycles`; once a wait of the CTA has given up (*abort), none waits
+// any more.  False: the phase is not complete.
+constexpr long long kWaitCycles = 1ll << 31;           // about a second
+__device__ __forceinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, int* abort, long long cycles) {
   const long long t0 = clock64();
   while (!mbar_try(bar, parity)) {
-    if (*static_cast<volatile int*>(abort)) return true;
-    if (clock64() - t0 > (1ll << 31)) {
+    if (*static_cast<volatile int*>(abort)) return false;
+    if (clock64() - t0 > cycles) {
       *static_cast<volatile int*>(abort) = 1;
       return false;
     }
@@ -301,8 +302,8 @@ __device__ __forceinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, i
   return true;
 }
 // The same with the usual case, a completed phase, inline (a clock read costs more than the test).
-__device__ __forceinline__ bool mbar_wait_timed(uint64_t* bar, uint32_t parity, int* abort) {
-  return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, abort);
+__device__ __forceinline__ bool mbar_wait_timed(uint64_t* bar, uint32_t parity, int* abort, long long cycles = kWaitCycles) {
+  return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, abort, cycles);
 }
 
 __device__ __forceinline__ float ex2(float x) {

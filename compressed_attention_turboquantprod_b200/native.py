@@ -83,6 +83,7 @@ def _load() -> ctypes.CDLL:
         "tq_debug_fail_next": (I, [ctypes.c_char_p]),
         "tq_debug_bounds_enabled": (I, []),
         "tq_debug_bounds_check": (I, []),
+        "tq_debug_paged_lose_copies": (I, [I]),
         "tq_codebook_build": (I, [I, I, P, P, P]),
         "tq_projections_workspace_bytes": (SZ, [I]),
         "tq_make_projections": (I, [I, I, I, U64, U64, P, P, P, P, SZ, P]),
@@ -560,6 +561,10 @@ def tq_debug_fail_next(name: Optional[str]):
 
 def tq_debug_bounds_enabled() -> int:
     return lib.tq_debug_bounds_enabled()
+
+
+def tq_debug_paged_lose_copies(on: bool):
+    _check(lib.tq_debug_paged_lose_copies(int(on)), "tq_debug_paged_lose_copies")
 
 
 def tq_debug_bounds_check():

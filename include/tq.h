@@ -740,6 +740,11 @@ int tq_sensitivity_profile(const double* layer_var, int L, int num_groups, int m
 int tq_debug_bounds_enabled(void);
 int tq_debug_bounds_check(void);
 
+/* Bounds-checked build only (else UNSUPPORTED), SYNCHRONOUS: while `on` is not 0 the copies of
+ * tq_paged_attention's decode are left out, as if their check had failed, so that its bounded
+ * waits run out (after a few hundredths of a second) and the status reports it. */
+int tq_debug_paged_lose_copies(int on);
+
 #ifdef __cplusplus
 }
 #endif
