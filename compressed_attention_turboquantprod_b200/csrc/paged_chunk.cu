@@ -162,6 +162,7 @@ template <int MT>
 struct ChunkShared {
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], q_free[2], o_free[2];
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];      // [row block][tile mod 2]
+  uint64_t done;                           // every product and arrival of the products' warp
   SplitPlan plan;
   float sk[4][4], lv[4][4];                // a tile's scales per 16 tokens: of the keys, log2 of the values' (or kZeros)
   float fr[2][128 * MT];                   // a row's factor on S, per query operand
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         mbar_init(&sh.pv_done[w][i], 1);
       }
     }
+    mbar_init(&sh.done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sh.abort = 0;
   }
@@ -490,6 +492,14 @@ __global__ void __launch_bounds__(128 * MT + 256, 1) k_paged_chunk(PGeom g, Page
         }
       }
     });
+    // Nobody waits for the last k_free and v_free, nor, once a wait has given up, for the products: none
+    // may be on its way when the tensor and shared memory go.
+    mma_commit_elected(&sh.done);
+    for (const long long t0 = clock64(); !mbar_try(&sh.done, 0);)
+      if (clock64() - t0 > kWaitCycles) {
+        atomicOr(&g.state->status, kPagedWait);
+        break;
+      }
   } else if (is_soft) {
     // =================================================================== softmax
     const uint32_t lrow = (uint32_t)(32 * (warp & 3)) << 16;
