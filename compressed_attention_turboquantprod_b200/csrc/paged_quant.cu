@@ -382,6 +382,11 @@ __global__ void __launch_bounds__(kWThreads) k_paged_read(PGeom g, int layer, co
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
   const int h = blockIdx.y, kv = blockIdx.z;
+  if (blockIdx.x == 0 && h == 0 && kv == 0) {
+    bool bad = false;
+    for (int r = tid; r < n; r += kWThreads) bad |= cu[r] < 0 || cu[r + 1] < cu[r] || cu[r + 1] > total;
+    if (bad) atomicOr(&g.state->status, kPagedBadOffsets);
+  }
   // the sequence and tile of this CTA: rows in groups of 32, one per lane
   int item = blockIdx.x, i = -1;
   for (int i0 = 0; i0 < n; i0 += 32) {
@@ -407,10 +412,7 @@ __global__ void __launch_bounds__(kWThreads) k_paged_read(PGeom g, int layer, co
   const int len = paged_len(g, slot);
   const int t0 = RT * item, nt = min(RT, count - t0);
   T* out = kv ? V : K;
-  if (c0 < 0 || (int64_t)c0 + count > total) {
-    if (tid == 0) atomicOr(&g.state->status, kPagedBadOffsets);
-    return;
-  }
+  if (c0 < 0 || (int64_t)c0 + count > total) return;
   // four codes to four outputs
   struct alignas(4 * sizeof(T)) Four {
     T e[4];

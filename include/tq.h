@@ -594,7 +594,10 @@ int tq_paged_append(tq_paged* c, const int32_t* slots, const int32_t* cu, int n,
  * tq_paged_read -- the first cu[i+1] - cu[i] cached tokens of slot slots[i] as
  * floats (code * scale rounded once to desc.dtype; zeros past the sequence's end)
  * into K, V [total][Hkv][d] at tokens cu[i].. .  Rows outside [cu[0], cu[n]) are
- * left as they were.  Errors: INVALID_ARG, CUDA.
+ * left as they were.
+ *   cu     device int32[n+1], cu[0] >= 0, not decreasing, cu[n] <= total
+ * Device checks: INVALID_ARG (offsets; a row that leaves the arrays is not read).
+ * Errors: INVALID_ARG, CUDA.
  */
 int tq_paged_read(const tq_paged* c, int layer, const int32_t* slots, const int32_t* cu, int n,
                   int64_t total, void* K, void* V, void* stream);

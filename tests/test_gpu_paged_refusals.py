@@ -145,3 +145,15 @@ def test_check_reports_every_reason_once():
         assert text in e.value.message
     assert c.check() == 4
     same_tables(c, m)
+
+
+@pytest.mark.parametrize("cu", [[0, 20, 10, 36], [0, 5, 5, 41], [-1, 5, 20, 36], [30, 20, 10, 0]])
+def test_a_read_with_bad_offsets_is_reported(cu):
+    from compressed_attention_turboquantprod_b200 import TQError
+    c, m = make(1, 64, 6, 3, 4, 16, "int8", "f16")
+    fill(c, m, [20, 16, 3], "f16", 95)
+    c.read(i32([0, 1, 2]), i32(cu), 40)
+    with pytest.raises(TQError) as e:
+        c.check()
+    assert e.value.status == nat().TQ_ERR_INVALID_ARG
+    same_values(c, m, "f16")
