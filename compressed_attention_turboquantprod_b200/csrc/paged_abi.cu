@@ -290,7 +290,8 @@ int tq_paged_attention(const tq_paged* c, int layer, const void* Q, int64_t q_st
   if (Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > tq::kMaxG)
     return set_error(TQ_ERR_UNSUPPORTED, "Hq=%d must be a multiple of Hkv=%d with at most %d heads per KV head", Hq, Hkv,
                      tq::kMaxG);
-  if (total_q < 0 || total_q > INT_MAX || max_q < 1 || max_q > (1 << 24))
+  // (a call without queries has no longest row)
+  if (total_q < 0 || total_q > INT_MAX || max_q < (total_q > 0 ? 1 : 0) || max_q > (1 << 24))
     return set_error(TQ_ERR_INVALID_ARG, "tq_paged_attention: total_q=%lld max_q=%d", (long long)total_q, max_q);
   if (!std::isfinite(softmax_scale)) return set_error(TQ_ERR_INVALID_ARG, "tq_paged_attention: softmax_scale not finite");
   if (total_q == 0) return tq::clear_error();

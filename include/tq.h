@@ -620,7 +620,8 @@ int tq_paged_table(const tq_paged* c, const int32_t* slots, int n, int32_t* out,
  *   Q        device, token t's heads [Hq][d] at element t * q_stride (16-byte
  *            aligned tokens, q_stride >= Hq * d), of desc.dtype
  *   Hq       a multiple of Hkv, at most 8 Hkv
- *   cu       device int32[n+1], not decreasing; max_q >= every cu[i+1] - cu[i]
+ *   cu       device int32[n+1], not decreasing; max_q >= every cu[i+1] - cu[i], at
+ *            least 1 (0 where total_q is 0: nothing is done then)
  *   total_q  tokens in Q and out; tokens outside [cu[0], cu[n]) are left as they were
  *   out      device [total_q][Hq][d] of desc.dtype (written); not over Q
  *   lse      device float[total_q][Hq]: log sum exp of the scaled logits (-inf where

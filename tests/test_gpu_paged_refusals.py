@@ -157,3 +157,15 @@ def test_a_read_with_bad_offsets_is_reported(cu):
         c.check()
     assert e.value.status == nat().TQ_ERR_INVALID_ARG
     same_values(c, m, "f16")
+
+
+def test_a_batch_without_queries():
+    c, m = make(1, 64, 6, 2, 4, 16, "int8", "f16")
+    fill(c, m, [20], "f16", 97)
+    Q = tokens(1, 2, 64, "f16", 98)
+    out = c.attend(Q[:0], i32([0, 1]), i32([0, 0, 0]), 0)
+    assert out.shape == (0, 2, 64) and c.check() == 4
+    c.append(Q[:0, :1], Q[:0, :1], i32([0, 1]), i32([0, 0, 0]))
+    K, V = c.read(i32([0, 1]), i32([0, 0, 0]), 0)
+    assert K.shape == V.shape == (0, 1, 64)
+    same_tables(c, m)

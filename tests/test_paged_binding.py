@@ -113,3 +113,18 @@ def test_append_refusals_of_the_library():
         native.tq_debug_fail_next(name)
         assert getattr(L, name)(ctypes.byref(c), *args) == native.TQ_ERR_CUDA
         assert L.tq_last_error() == b"injected fault"
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="uses fake device pointers")
+def test_attention_without_queries():
+    """The longest of no rows is 0."""
+    native = importlib.import_module("compressed_attention_turboquantprod_b200.native")
+    fake = ctypes.c_void_p(1 << 20)
+    c = native.tq_paged_layout(native.make_paged_desc(1, 2, 64, 16, 10, 4, 5, torch.bfloat16, 0))
+    c.base = 1 << 20
+
+    def attention(max_q, total):
+        return native.lib.tq_paged_attention(ctypes.byref(c), 0, None, 256, 4, fake, fake, 1, max_q, total, 1, 0.1, None, None,
+                                             fake, 1 << 40, None)
+    assert attention(0, 0) == native.TQ_OK and attention(5, 0) == native.TQ_OK
+    assert attention(-1, 0) == native.TQ_ERR_INVALID_ARG and attention(0, 1) == native.TQ_ERR_INVALID_ARG
