@@ -28,6 +28,16 @@ int check_pending(const char* where) {
 
 int done(cudaError_t e, const char* where) { return e == cudaSuccess ? tq::clear_error() : cuda_fail(e, where); }
 
+// Whether two arrays share bytes.
+struct Extent {
+  const void* p;
+  int64_t bytes;
+};
+bool meet(const Extent& a, const Extent& b) {
+  const char *x = static_cast<const char*>(a.p), *y = static_cast<const char*>(b.p);
+  return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 int layout_status(const tq_paged_desc* d, tq_paged* out) {
@@ -248,6 +258,10 @@ int tq_paged_read(const tq_paged* c, int layer, const int32_t* slots, const int3
   if (total == 0) return tq::clear_error();
   if (!K || !V || !aligned(K, 16) || !aligned(V, 16))
     return set_error(TQ_ERR_INVALID_ARG, "tq_paged_read: K and V must be non-null, 16-byte aligned");
+  const int64_t bytes = total * c->desc.Hkv * c->desc.d * tq::paged_esize(c->desc.dtype);
+  const Extent k{K, bytes}, v{V, bytes}, m{c->base, (int64_t)c->bytes};
+  if (meet(k, v) || meet(k, m) || meet(v, m))
+    return set_error(TQ_ERR_INVALID_ARG, "tq_paged_read: K, V and the cache overlap");
   st = check_pending("tq_paged_read");
   if (st != TQ_OK) return st;
   return done(tq::paged_launch_read(geom(c), layer, slots, cu, n, total, K, V, static_cast<cudaStream_t>(stream)),
@@ -300,11 +314,14 @@ int tq_paged_attention(const tq_paged* c, int layer, const void* Q, int64_t q_st
   if (bad_stride(c, q_stride, Hq))
     return set_error(TQ_ERR_INVALID_ARG, "tq_paged_attention: q_stride=%lld: at least Hq * d, a multiple of 16 bytes",
                      (long long)q_stride);
-  // several CTAs read a query that one of them answers: the output may not lie over the queries
+  // several CTAs read a query, and the codes, that one of them answers: nothing that is written may lie
+  // over what is read
   const int64_t es = tq::paged_esize(c->desc.dtype), row = (int64_t)Hq * c->desc.d * es;
-  const char *qb = static_cast<const char*>(Q), *ob = static_cast<const char*>(out);
-  if (ob < qb + (total_q - 1) * q_stride * es + row && qb < ob + total_q * row)
-    return set_error(TQ_ERR_INVALID_ARG, "tq_paged_attention: out overlaps Q");
+  const Extent q{Q, (total_q - 1) * q_stride * es + row}, o{out, total_q * row}, l{lse, total_q * Hq * 4},
+      w{workspace, (int64_t)tq::paged_attn_ws_bytes(c->desc.d)}, m{c->base, (int64_t)c->bytes};
+  if (meet(o, q) || meet(o, l) || meet(o, w) || meet(o, m) || meet(l, q) || meet(l, w) || meet(l, m) || meet(w, q) ||
+      meet(w, m))
+    return set_error(TQ_ERR_INVALID_ARG, "tq_paged_attention: out, lse or workspace overlaps another array");
   if (!workspace || !aligned(workspace, 256) || ws_bytes < tq::paged_attn_ws_bytes(c->desc.d))
     return set_error(TQ_ERR_INVALID_ARG, "tq_paged_attention: workspace must be 256-byte aligned, %zu bytes",
                      tq::paged_attn_ws_bytes(c->desc.d));

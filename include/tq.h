@@ -596,6 +596,7 @@ int tq_paged_append(tq_paged* c, const int32_t* slots, const int32_t* cu, int n,
  * into K, V [total][Hkv][d] at tokens cu[i].. .  Rows outside [cu[0], cu[n]) are
  * left as they were.
  *   cu     device int32[n+1], cu[0] >= 0, not decreasing, cu[n] <= total
+ *   K, V   not over each other or the cache
  * Device checks: INVALID_ARG (offsets; a row that leaves the arrays is not read).
  * Errors: INVALID_ARG, CUDA.
  */
@@ -623,7 +624,8 @@ int tq_paged_table(const tq_paged* c, const int32_t* slots, int n, int32_t* out,
  *   cu       device int32[n+1], not decreasing; max_q >= every cu[i+1] - cu[i], at
  *            least 1 (0 where total_q is 0: nothing is done then)
  *   total_q  tokens in Q and out; tokens outside [cu[0], cu[n]) are left as they were
- *   out      device [total_q][Hq][d] of desc.dtype (written); not over Q
+ *   out      device [total_q][Hq][d] of desc.dtype (written).  out, lse and workspace may not
+ *            lie over each other, Q or the cache
  *   lse      device float[total_q][Hq]: log sum exp of the scaled logits (-inf where
  *            nothing is visible), or NULL
  *   workspace  device, 256-byte aligned, tq_paged_workspace_bytes(c) bytes, made

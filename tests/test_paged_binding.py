@@ -128,3 +128,38 @@ def test_attention_without_queries():
                                              fake, 1 << 40, None)
     assert attention(0, 0) == native.TQ_OK and attention(5, 0) == native.TQ_OK
     assert attention(-1, 0) == native.TQ_ERR_INVALID_ARG and attention(0, 1) == native.TQ_ERR_INVALID_ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="uses fake device pointers")
+def test_arrays_that_overlap():
+    """Apart, the calls come as far as the missing GPU; over one another they are refused before."""
+    native = importlib.import_module("compressed_attention_turboquantprod_b200.native")
+    L, bad = native.lib, native.TQ_ERR_INVALID_ARG
+    c = native.tq_paged_layout(native.make_paged_desc(1, 2, 64, 16, 10, 4, 5, torch.bfloat16, 0))
+    c.base = 1 << 30
+    ws = L.tq_paged_workspace_bytes(ctypes.byref(c))
+    at = dict(base=1 << 30, q=2 << 30, out=3 << 30, lse=4 << 30, ws=5 << 30, k=6 << 30, v=7 << 30)
+    row = 4 * 64 * 2
+
+    def attention(**kw):
+        a = {**at, **kw}
+        c.base = a["base"]
+        return L.tq_paged_attention(ctypes.byref(c), 0, a["q"], 512, 4, at["k"], at["v"], 1, 9, 9, 1, 0.1, a["out"], a["lse"],
+                                    a["ws"], ws, None)
+
+    def read(**kw):
+        a = {**at, **kw}
+        c.base = a["base"]
+        return L.tq_paged_read(ctypes.byref(c), 0, at["q"], at["q"], 1, 9, a["k"], a["v"], None)
+    end = {"base": (1 << 30) + c.bytes, "q": (2 << 30) + 8 * 1024 + row, "out": (3 << 30) + 9 * row, "lse": (4 << 30) + 9 * 16,
+           "ws": (5 << 30) + ws, "k": (6 << 30) + 9 * 256}
+    assert attention() == native.TQ_ERR_CUDA and attention(lse=None) == native.TQ_ERR_CUDA
+    for a, b in (("out", "q"), ("out", "lse"), ("out", "ws"), ("out", "base"), ("lse", "q"), ("lse", "ws"), ("lse", "base"),
+                 ("ws", "q"), ("ws", "base")):
+        up = lambda x: -(-x // 256) * 256
+        assert attention(**{a: at[b]}) == bad, (a, b)
+        assert attention(**{a: up(end[b] - 255) if a != "lse" else end[b] - 4}) == bad or up(end[b] - 255) >= end[b], (a, b)
+        assert attention(**{a: up(end[b])}) == native.TQ_ERR_CUDA, (a, b)
+    assert read() == native.TQ_ERR_CUDA and read(k=end["k"], v=at["k"]) == native.TQ_ERR_CUDA
+    for kw in (dict(v=at["k"]), dict(v=end["k"] - 16), dict(k=at["base"]), dict(v=end["base"] - 256)):
+        assert read(**kw) == bad, kw
