@@ -41,8 +41,8 @@ constexpr int kTile = 64;
 // tensor core's own long sums truncate: 2^-25 a step, one way).
 //
 // Measured (one B200, copy peak 6466 GB/s): 8 sequences of 32768 tokens, 32 / 8 heads, d = 128, int8:
-// 101 us for 537 MB, 0.82 of the peak, DRAM traffic 1.02 of that; d = 256, e4m3, 223 k tokens of 4 heads:
-// 92 us, 0.77.  One sequence of 517 tokens: 15 us, a chain of about ten dependent loads and the first
+// 97 us for 537 MB, 0.86 of the peak, DRAM traffic 1.02 of that; d = 256, e4m3, 223 k tokens of 4 heads:
+// 90 us, 0.79.  One sequence of 517 tokens: 15 us, a chain of about ten dependent loads and the first
 // fetch of the code.  What bounds the long ones is latency within a warp: 8 warps an SM (4 at d = 256) at
 // 44 % issue, as many as 240 registers allow; three CTAs at d = 64 (143 registers) gained nothing.
 constexpr int kDecWarps = 4;
@@ -604,10 +604,15 @@ cudaError_t paged_launch_ws_init(void* ws, cudaStream_t s) {
 
 cudaError_t paged_launch_attention(const PGeom& g, const PagedAttn& a, cudaStream_t s) {
   // Up to 24 query rows of a KV head the decode, which reads the codes once for every 8 rows, is the
-  // faster; the chunk kernel's time does not depend on the rows up to 128.  Measured with G = 4, d = 128, 8
-  // sequences, decode and chunk in us: 32768 tokens 12-16 rows 173 / 280, 24 rows 250 / 280, 32 rows 331 /
-  // 279; 2000 tokens 16 rows 33 / 36, 24 rows 39 / 36, 32 rows 45 / 36.  fp32 stays with the decode, whose
-  // split halves keep its precision.
+  // faster; the chunk kernel's time does not depend on the rows up to 128.  Measured on 8 sequences, G = 4,
+  // int8, decode / chunk in us:
+  //                          16 rows     24 rows     32 rows
+  //   d = 128, 32768 tokens  170 / 290   270 / 290   356 / 292        2000 tokens  26 / 39   31 / 38   37 / 38
+  //   d = 64,  32768         115 / 243   167 / 243   218 / 241        2000         19 / 30   22 / 30   27 / 29
+  //   d = 256, 32768         222 / 259   320 / 259   421 / 258        2000         32 / 45   36 / 45   45 / 45
+  // (e4m3, d = 256 263 / 257 at 24 rows; G = 1, 8 as G = 4 at d = 128.)  One limit for all: away from d = 128
+  // it is off by one group of 8 rows and costs 10 % (d = 64, 32 rows) to 24 % (d = 256, 24 rows) there.
+  // fp32 stays with the decode, whose split halves keep its precision.
   if (a.max_q * (a.Hq / g.Hkv) > 24 && g.dtype != TQ_F32) return paged_launch_chunk(g, a, s);
   if (g.d == 64) return decode_d<64>(g, a, s);
   if (g.d == 128) return decode_d<128>(g, a, s);

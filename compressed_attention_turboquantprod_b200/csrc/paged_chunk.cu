@@ -25,11 +25,12 @@
 // bits or exactly (bf16, f16 entries have at most 11 bits; q is scaled by a power of two per row).
 //
 // Measured (one B200, bf16 peak 1644 TFLOP/s): 64 queries on each of 8 x 32768 tokens, 32 / 8 heads, d =
-// 128, int8: 341 us, 806 TFLOP/s; prompts of 8192 and 6001 tokens on themselves, e4m3: 1006 us, 840
-// TFLOP/s.  A tile of 64 tokens takes about 2050 cycles where its products need 1280 and its exponentials
-// 1024.  The limit is the shared issue of 16 warps in four roles, each near its own serial time: leaving out
-// the exponentials, the expansion, the products or the loads alone gains 2, 0, 10 and 7 %, all four together
-// 43 %.  Tried in the states of the time: T = 128 with one S a row block took 3.0 ms on the prompts (each softmax waited for its own
+// 128, int8: 350 us, 786 TFLOP/s; prompts of 8192 and 6001 tokens on themselves, e4m3: 1021 us, 827
+// TFLOP/s.  A tile of 64 tokens takes about 2050 cycles on the prompts, whose codes come from L2, and about
+// 2400 on the long caches, where its products need 1280 and its exponentials 1024.  The limit is the shared
+// issue of 16 warps in four roles, each near its own serial time: leaving out the exponentials, the
+// expansion, the products or the loads alone gained 2, 0, 10 and 7 %, all four together 43 % (before the
+// folding of O and the reference R, which cost 3 and 2 %).  Tried in the states of the time: T = 128 with one S a row block took 3.0 ms on the prompts (each softmax waited for its own
 // products), S single and P apart 1.06 ms, products from a branch of one thread 3.2 ms, two converters
 // for the keys and two for the values 1.04 ms, requests into L2 four tiles ahead 1.03 ms.
 #include "paged_split.cuh"
@@ -839,8 +840,9 @@ template <int D>
 cudaError_t chunk_d(const PGeom& g, const PagedAttn& a, cudaStream_t s) {
   const bool i8 = g.code == TQ_CODE_INT8;
   if constexpr (chunk_max_mt<D>() == 2) {
-    // one row block where no sequence has more rows than it holds (128 rows over 8 x 32768 tokens, G = 4, d =
-    // 128: 277 us, with two blocks 328; 256 rows: 533 us in ones, 316 in twos)
+    // one row block where no sequence has more rows than it holds.  Measured with one block and with two, in
+    // us, for 128 and 256 rows of a head: 8 x 32768 tokens, 8 heads, int8, d = 128 284 / 332 and 567 / 346, d =
+    // 64 236 / 278 and 464 / 259; 8 x 1200 tokens, 16 heads, d = 64 30 / 39 and 45 / 39
     if ((int64_t)a.max_q * (a.Hq / g.Hkv) > 128)
       return i8 ? chunk_t<D, TQ_CODE_INT8, 2>(g, a, s) : chunk_t<D, TQ_CODE_E4M3, 2>(g, a, s);
   }

@@ -618,6 +618,9 @@ int tq_paged_table(const tq_paged* c, const int32_t* slots, int n, int32_t* out,
  * out = sum_t p_t v_t, p = softmax(softmax_scale <q, k_t>) over the visible tokens;
  * a query that sees none gives 0, one with a NaN or an infinity gives NaN (and a NaN
  * lse).  One query per sequence is the decode.
+ * Logits, the softmax's sums and the products' sums are held in fp32, p to 22 bits;
+ * in a bf16 or f16 call whose max_q * Hq / Hkv is above 24, p is rounded to f16 (11
+ * bits, one rounding a weight, against a weights' sum of the unrounded ones).
  *   Q        device, token t's heads [Hq][d] at element t * q_stride (16-byte
  *            aligned tokens, q_stride >= Hq * d), of desc.dtype
  *   Hq       a multiple of Hkv, at most 8 Hkv
