@@ -169,3 +169,66 @@ def test_a_batch_without_queries():
     K, V = c.read(i32([0, 1]), i32([0, 0, 0]), 0)
     assert K.shape == V.shape == (0, 1, 64)
     same_tables(c, m)
+
+
+@pytest.mark.parametrize("d,G,nq,lens", [(64, 1, 40, [700, 90]), (128, 4, 70, [9000, 300]), (256, 2, 33, [400, 17000])])
+def test_chunks_at_once_and_captured(d, G, nq, lens):
+    """Chunk calls on two streams at a time, and two graphs of them replayed on both: each has a workspace of
+    its own; at d = 64 their CTAs share SMs, and so wait for each other's tensor memory."""
+    c, m = make(2, d, 400, 2, 300, 64, "int8", "bf16")
+    fill(c, m, lens, "bf16", 101)
+    rows, cu = i32([0, 1]), offsets([nq, nq])
+    Q = [tokens(2 * nq, 2 * G, d, "bf16", 102 + i, 0.3) for i in range(2)]
+
+    def call(i):
+        return c.attend(Q[i], rows, cu, nq, causal=i == 0)
+    want = [call(0), call(1)]
+    if d != 128:
+        check_attention(c, m, Q[0], [0, 1], [nq, nq], True, "bf16", single_p=True)
+    st, got, graphs = [torch.cuda.Stream() for _ in range(2)], [], []
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(st[i]):
+                got.append((i, call(i)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call(i)
+        graphs.append((g, out))
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(st[i]):
+                graphs[i][1].zero_()
+                graphs[i][0].replay()
+        torch.cuda.synchronize()
+        got += [(i, graphs[i][1].clone()) for i in range(2)]
+    torch.cuda.synchronize()
+    for i, g in got:
+        assert torch.equal(g, want[i])
+    c.check()
+
+
+def test_captured_appends_with_padding_rows():
+    """A padded batch: offsets and slots change between replays, rows come and go as padding."""
+    c, m = make(2, 128, 60, 4, 12, 32, "e4m3", "bf16")
+    dirty(c, m, "bf16")
+    K, V = (torch.zeros(64, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    slots, cu = i32([-1] * 4), i32([0] * 5)
+    c.append(K, V, slots, cu)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.append(K, V, slots, cu)
+    for step, (s, counts) in enumerate((([2, -1, 0, 1], [30, 4, 1, 20]), ([3, 0, -1, -1], [33, 1, 9, 9]), ([-1] * 4, [0] * 4),
+                                        ([1, 2, 3, 0], [1, 1, 1, 61]))):
+        k, v = (tokens(64, 2, 128, "bf16", 110 + 2 * step + j) for j in range(2))
+        K.copy_(k), V.copy_(v), slots.copy_(i32(s)), cu.copy_(offsets(counts))
+        g.replay()
+        at = 0
+        for slot, n in zip(s, counts):
+            if slot >= 0:
+                m.append(slot, [(host(k[at:at + n]), host(v[at:at + n]))])
+            at += n
+        same_tables(c, m)
+        same_values(c, m, "bf16")
