@@ -311,10 +311,10 @@ class PagedKVCache:
         queries = native.check_queries(self.state, Q, slots, cu)
         if Q.dtype != self.dtype:
             raise ValueError(f"expected {self.dtype}, got {Q.dtype}")
-        if out is not None and (out.shape != Q.shape or out.dtype != self.dtype):
-            raise ValueError("out must have Q's shape and dtype")
-        if lse is not None and (lse.shape != Q.shape[:2] or lse.dtype != torch.float32):
-            raise ValueError("lse must be float32 [tokens, Hq]")
+        if out is not None and (out.shape != Q.shape or out.dtype != self.dtype or not out.is_contiguous()):
+            raise ValueError("out must be contiguous, of Q's shape and dtype")
+        if lse is not None and (lse.shape != Q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()):
+            raise ValueError("lse must be contiguous float32 [tokens, Hq]")
         return self._on(Q, slots, cu, out, lse, workspace), queries
 
     def attend(self, Q: torch.Tensor, slots: torch.Tensor, cu: torch.Tensor, max_q: int,
@@ -360,6 +360,8 @@ class PagedKVCache:
         """append() one token per slot (K, V [n, Hkv, d]), then decode().  What can be said of Q
         without the library is checked before the append."""
         cu = self._ones(slots.numel()) if cu is None else cu
+        if softmax_scale is not None and not math.isfinite(softmax_scale):
+            raise ValueError(f"softmax_scale {softmax_scale} is not finite")
         on, queries = self._queries(Q, slots, cu, out, lse, workspace)
         with on:
             self.append(K, V, slots, cu)

@@ -83,7 +83,8 @@ def test_a_decode_step_is_checked_before_its_append(cache):
     Q, out = (on(z(1, 4, 64, dtype=bf)) for _ in range(2))
     for q, kw in ((on(z(1, 4, 32, dtype=bf)), {}), (on(z(1, 4, 64)), {}), (on(z(4, 64, dtype=bf)), {}),
                   (z(1, 4, 64, dtype=bf), {}), (Q, dict(out=on(z(1, 4, 64)))), (Q, dict(lse=on(z(1, 3)))),
-                  (Q, dict(workspace=z(64)))):
+                  (Q, dict(workspace=z(64))), (Q, dict(out=on(z(1, 4, 128, dtype=bf))[..., ::2])),
+                  (Q, dict(lse=on(z(1, 8))[:, ::2])), (Q, dict(softmax_scale=float("nan")))):
         with pytest.raises(ValueError):
             cache.decode_step(K, K, q, slots, cu, **{**dict(out=out, workspace=ws), **kw})
         assert cache.calls == []
