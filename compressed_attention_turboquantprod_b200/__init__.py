@@ -363,6 +363,11 @@ class PagedKVCache:
         if softmax_scale is not None and not math.isfinite(softmax_scale):
             raise ValueError(f"softmax_scale {softmax_scale} is not finite")
         on, queries = self._queries(Q, slots, cu, out, lse, workspace)
+        _, heads, at, stride, _ = queries
+        if heads % self.desc.Hkv or not 1 <= heads // self.desc.Hkv <= 8:
+            raise ValueError(f"{heads} query heads over {self.desc.Hkv} KV heads")
+        if at % 16 or stride * Q.element_size() % 16 or (out is not None and out.data_ptr() % 16):
+            raise ValueError("Q's tokens and out must be 16-byte aligned")
         with on:
             self.append(K, V, slots, cu)
             return self._attend(queries, Q, slots, cu, 1, True, softmax_scale, layer, out, lse,

@@ -84,6 +84,9 @@ def test_a_decode_step_is_checked_before_its_append(cache):
     for q, kw in ((on(z(1, 4, 32, dtype=bf)), {}), (on(z(1, 4, 64)), {}), (on(z(4, 64, dtype=bf)), {}),
                   (z(1, 4, 64, dtype=bf), {}), (Q, dict(out=on(z(1, 4, 64)))), (Q, dict(lse=on(z(1, 3)))),
                   (Q, dict(workspace=z(64))), (Q, dict(out=on(z(1, 4, 128, dtype=bf))[..., ::2])),
+                  (on(z(1, 3, 64, dtype=bf)), dict(out=on(z(1, 3, 64, dtype=bf)))),
+                  (on(z(1, 18, 64, dtype=bf)), dict(out=on(z(1, 18, 64, dtype=bf)))),
+                  (on(z(260, dtype=bf))[4:].view(1, 4, 64), {}), (Q, dict(out=on(z(260, dtype=bf))[4:].view(1, 4, 64))),
                   (Q, dict(lse=on(z(1, 8))[:, ::2])), (Q, dict(softmax_scale=float("nan")))):
         with pytest.raises(ValueError):
             cache.decode_step(K, K, q, slots, cu, **{**dict(out=out, workspace=ws), **kw})
