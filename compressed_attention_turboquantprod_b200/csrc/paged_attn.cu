@@ -41,7 +41,7 @@ constexpr int kTile = 64;
 // tensor core's own long sums truncate: 2^-25 a step, one way).
 //
 // Measured (one B200, copy peak 6466 GB/s): 8 sequences of 32768 tokens, 32 / 8 heads, d = 128, int8:
-// 97 us for 537 MB, 0.86 of the peak, DRAM traffic 1.02 of that; d = 256, e4m3, 223 k tokens of 4 heads:
+// 97-102 us on different cards for 537 MB, 0.82-0.86 of the peak, DRAM traffic 1.02 of that; d = 256, e4m3, 223 k tokens of 4 heads:
 // 90 us, 0.79.  One sequence of 517 tokens: 15 us, a chain of about ten dependent loads and the first
 // fetch of the code.  What bounds the long ones is latency within a warp: 8 warps an SM (4 at d = 256) at
 // 44 % issue, as many as 240 registers allow; three CTAs at d = 64 (143 registers) gained nothing.
